@@ -251,7 +251,7 @@ def _own(s, op):
         ssu.delta_prefill(s["call"])
         return dict(out=s["out"], final=s["final"])
     if op == "step":
-        ssu.delta_step(s["dc"], s["call"])
+        ssu.delta_replay_step(s["dc"], s["call"])
         return dict(out=s["out"], k_cache=s["cache"]["k_cache"], v_cache=s["cache"]["v_cache"], gate_cache=s["cache"]["gate_cache"])
     if op == "flush":
         ssu.delta_flush(s["dc"], s["ids"], s["fold"])
