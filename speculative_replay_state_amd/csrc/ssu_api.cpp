@@ -12,9 +12,29 @@
 #include "../../include/ssu.h"
 #include "ssu_internal.h"
 
+namespace ssu {
+
+static thread_local char g_err[512] = "";
+
+int api_fail(int code, const char *fmt, ...) {
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(g_err, sizeof g_err, fmt, ap);
+  va_end(ap);
+  return code;
+}
+
+int api_ok() {
+  g_err[0] = '\0';
+  return 0;
+}
+
+}  // namespace ssu
+
 namespace {
 
-thread_local char g_err[512] = "";
+constexpr auto &fail = ssu::api_fail;
+constexpr auto &ok = ssu::api_ok;
 
 // Default AUTO crossover in work units (batch * nheads).  On MI355X the
 // monolith is faster than the split at every measured size (128 to 65536
@@ -24,19 +44,6 @@ thread_local char g_err[512] = "";
 // wave costs less than the split's extra launch and scratch round trip.  AUTO
 // therefore never picks the split unless a caller lowers the threshold.
 std::atomic<int64_t> g_split_threshold{INT64_MAX};
-
-int fail(int code, const char *fmt, ...) {
-  va_list ap;
-  va_start(ap, fmt);
-  vsnprintf(g_err, sizeof g_err, fmt, ap);
-  va_end(ap);
-  return code;
-}
-
-int ok() {
-  g_err[0] = '\0';
-  return SSU_OK;
-}
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
@@ -248,7 +255,7 @@ int resolve(const ssu_cache *c, const ssu_step *s) {
 
 extern "C" {
 
-const char *ssu_last_error(void) { return g_err; }
+const char *ssu_last_error(void) { return ssu::g_err; }
 
 int64_t ssu_get_split_threshold(void) { return g_split_threshold.load(); }
 

@@ -85,4 +85,10 @@ hipError_t launch_flush(const KCache &c, const int32_t *slot_idx, const int32_t 
 hipError_t launch_init(const KCache &c, const float *states, int64_t states_stride,
                        const int32_t *slot_idx, int n, int state_type, hipStream_t stream);
 
+// The calling thread's error message (ssu_last_error), set by every entry
+// point: api_fail formats it and returns `code`, api_ok clears it and returns
+// SSU_OK.
+int api_fail(int code, const char *fmt, ...) __attribute__((format(printf, 2, 3)));
+int api_ok();
+
 }  // namespace ssu
