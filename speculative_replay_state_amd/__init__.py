@@ -6,6 +6,12 @@ tensors and calls the library.  Every step of the computation runs in the
 library's HIP kernels.  Importing fails loudly when libssu.so has not been
 built (python speculative_replay_state_amd/build.py); there is no fallback.
 
+The gated delta rule (include/ssu_delta.h) and the verification of drafted
+tokens (include/ssu_verify.h) are bound in delta.py and verification.py; their
+front ends (DeltaCache, make_delta_step, delta_replay_step, delta_flush,
+make_delta_prefill, delta_prefill, make_verify, verify, ...) are names of
+this package too.
+
 Names follow the C ABI: ssu_init_state, ssu_replay_step, ssu_flush,
 ssu_workspace_size, ssu_resolve_algo, ssu_last_error, plus DeviceCache (the
 device tensors of one cache, in the layout of ssu_cache) and replay_step /
@@ -342,3 +348,11 @@ def flush(cache: DeviceCache, slot_idx, num_fold, A, stream=None, sr_seed=0):
     _packed(A, "A", 4 * cache.nheads)
     _check(ssu_flush(cache.desc(), _ptr(slot_idx), _ptr(num_fold), _ptr(A), slot_idx.numel(), int(sr_seed),
                      _stream(stream)))
+
+
+# the gated delta rule and the verification of drafted tokens
+from .delta import (  # noqa: E402
+    SSU_DELTA_MAX_PAIRS, DeltaCache, SsuDeltaCache, SsuDeltaPrefill, SsuDeltaStep, delta_flush, delta_init_state,
+    delta_prefill, delta_prefill_workspace_size, delta_read_state, delta_replay_step, make_delta_prefill, make_delta_step)
+from .verification import (  # noqa: E402
+    SSU_STATUS_BAD_PROBS, SSU_STATUS_BAD_TOKEN, SsuVerify, make_verify, verify, verify_workspace_size)

@@ -4,9 +4,10 @@
 
 (run as a script: importing the package fails until the library exists)
 
-Compiles the device code (csrc/ssu_kernels.cuh through ssu_kernels_inst.hip,
-once per state type, in parallel), the dispatch (csrc/ssu_launch.cpp) and the
-host entry points (csrc/ssu_api.cpp), and links them into
+Compiles the device code in parallel (csrc/ssu_kernels.cuh and
+csrc/delta_kernels.cuh through their *_inst.hip, once per state type;
+delta_prefill.hip; verify_kernels.hip), the dispatch (csrc/ssu_launch.cpp)
+and the host entry points (csrc/*_api.cpp), and links them into
 speculative_replay_state_amd/libssu.so.
 """
 from __future__ import annotations
@@ -57,8 +58,15 @@ def build(verbose: bool = False) -> str:
             objs.append(o)
             jobs.append([hipcc, "--offload-arch=" + ARCH, *COMMON, "-DSSU_INST_ST=%d" % st, "-c",
                          os.path.join(CSRC, "ssu_kernels_inst.hip"), "-o", o])
-        for src in ("ssu_launch.cpp", "ssu_api.cpp"):
-            o = os.path.join(tmp, src.replace(".cpp", ".o"))
+        # the gated delta rule's, once per checkpoint type it has
+        for st in range(3):
+            o = os.path.join(tmp, "delta_kernels_%d.o" % st)
+            objs.append(o)
+            jobs.append([hipcc, "--offload-arch=" + ARCH, *COMMON, "-DSSU_INST_ST=%d" % st, "-c",
+                         os.path.join(CSRC, "delta_kernels_inst.hip"), "-o", o])
+        for src in ("delta_prefill.hip", "verify_kernels.hip", "ssu_launch.cpp", "ssu_api.cpp", "delta_api.cpp",
+                    "verify_api.cpp"):
+            o = os.path.join(tmp, os.path.splitext(src)[0] + ".o")
             objs.append(o)
             jobs.append([hipcc, "--offload-arch=" + ARCH, *COMMON, "-x", "hip", "-c", os.path.join(CSRC, src),
                          "-o", o])
