@@ -11,9 +11,8 @@
  *   S <- exp(g_t) S;  u_t = b_t (v_t - S k^_t);  S <- S + u_t k^_t^T
  *   o_t = scale S q^_t
  * Everything between the inputs and the outputs is computed in fp32 (decay
- * sums in fp64), matrix products from operands split into bf16 parts: three
- * (24 bits) towards fp32 results, two (16 bits) towards bf16 outputs and
- * 16-bit checkpoints.  Infinities or NaN in a token's inputs may reach every
+ * sums in fp64); matrix products take operands that are not bf16 in two or
+ * three bf16 parts: fp32 states and outputs end within 1e-6 of their norm.  Infinities or NaN in a token's inputs may reach every
  * output of the call for its request and head (the tokens before it in the
  * call too), and nothing else.
  *
@@ -149,7 +148,8 @@ int ssu_delta_read_state(const ssu_delta_cache *cache, float *states, int64_t st
  * sequence whose cu_seqlens are negative, decreasing or past rows is skipped
  * and ORs SSU_STATUS_BAD_SEQLEN into *status (when not NULL).
  * Requirements: dim_k, dim_v and the heads as in ssu_delta_cache; rows *
- * nheads_v <= 2^30; num_seqs * nheads_v <= SSU_DELTA_MAX_PAIRS.  num_seqs == 0
+ * nheads_v <= 2^30; num_seqs * nheads_v <= SSU_DELTA_MAX_PAIRS; nheads_v *
+ * dim_v and the row strides below 2^23 elements.  num_seqs == 0
  * is a no-op; with rows == 0 the per-row tensors may be NULL.
  */
 typedef struct ssu_delta_prefill_args {

@@ -266,6 +266,9 @@ int ssu_delta_prefill(const ssu_delta_prefill_args *a, hipStream_t stream) {
     return api_fail(SSU_ERR_INVALID, "initial_states and final_states must be 16-byte aligned");
   rc = check_inputs(a, a->rows > 0, a->nheads_k, a->nheads_v, a->dim_k, a->dim_v);
   if (rc != SSU_OK) return rc;
+  const int64_t wide = (int64_t)1 << 23;  // a chunk's rows are addressed with 32-bit byte offsets
+  if ((int64_t)a->nheads_v * a->dim_v >= wide || a->q_row_stride >= wide || a->k_row_stride >= wide || a->v_row_stride >= wide)
+    return api_fail(SSU_ERR_UNSUPPORTED, "nheads_v x dim_v and the row strides must be below 2^23 elements");
   const size_t need = prefill_bytes(a->rows, a->num_seqs, a->nheads_v);
   if (!a->workspace || a->workspace_bytes < need)
     return api_fail(SSU_ERR_WORKSPACE, "the prefill needs a workspace of %zu bytes (got %zu%s)", need, a->workspace_bytes,

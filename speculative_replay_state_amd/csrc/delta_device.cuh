@@ -1,8 +1,8 @@
 // Device pieces shared by the kernels of the gated delta rule.
 //
 // A window of w tokens with gates g_s, b_s and running sums G_s = g_0 + .. +
-// g_s (fp64: exp(G_i - G_j) is wanted to fp32 accuracy while |G| grows with
-// the window) acts on a state S [dim_v][dim_k] as
+// g_s (fp64 and in units of ln 2: e^(G_i - G_j), one v_exp_f32, is wanted to
+// fp32 accuracy while |G| grows with the window) acts on a state S [dim_v][dim_k] as
 //   A_ij = b_i e^(G_i - G_j) k^_i . k^_j  (j < i),   T = (I + A)^-1,
 //   U = T b (V - e^G K^ S^T),
 //   o_i = scale (e^(G_i) S q^_i + sum_(j <= i) e^(G_i - G_j) (q^_i . k^_j) u_j),
@@ -96,6 +96,7 @@ __device__ __forceinline__ void split(const float (&x)[E], V (&out)[NP]) {
     for (int i = 0; i < E / 2; ++i) {
       o.w[i] = pack_bf16(rest[2 * i], rest[2 * i + 1]);
       if (p + 1 < NP) {
+        asm("" : "+v"(o.w[i]));  // else the compiler converts the lower value a second time
         rest[2 * i] -= bf2f(o.w[i] & 0xFFFFu);
         rest[2 * i + 1] -= __uint_as_float(o.w[i] & 0xFFFF0000u);
       }
@@ -153,37 +154,18 @@ __device__ __forceinline__ float2 delta_gate(float dt, float beta, float A, floa
   return r;
 }
 
-// The tokens of a window as the kernels keep them in LDS (one wave's).
-template <int KW, int DK>
+constexpr double kLog2e = 1.4426950408889634;
+__device__ __forceinline__ float exp2_d(double x) { return __builtin_amdgcn_exp2f((float)x); }
+
+// What the kernels keep of a window in LDS (one wave's).
+template <int KW>
 struct WinLds {
-  static constexpr int kKS = DK + 8;  // row stride: 8 values on, so 16 rows start in different banks
   static constexpr int kAS = KW + 4;
   double G[KW];
   __align__(16) float A[KW * kAS];  // A, later T's diagonal blocks over its own (row major)
   float b[KW];
   float rk[KW];
-  uint16_t k[KW * kKS];
 };
-
-// S_ij = k_i . k_j of the window from its LDS rows: tile (ti, tj <= ti) at
-// index ti (ti + 1) / 2 + tj, lane (m, q) rows 16 ti + 4 q + r, column 16 tj + m.
-template <int KW, int DK>
-__device__ __forceinline__ void gram_kk(const WinLds<KW, DK> &w, int lane, f32x4 (&s)[KW / 16 * (KW / 16 + 1) / 2]) {
-  const int m = lane & 15, q = lane >> 4;
-#pragma unroll
-  for (int i = 0; i < KW / 16 * (KW / 16 + 1) / 2; ++i) s[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-  for (int u = 0; u < DK / 32; ++u) {
-    bf16x8 f[KW / 16];
-#pragma unroll
-    for (int t = 0; t < KW / 16; ++t)
-      f[t] = __builtin_bit_cast(bf16x8, ld16(w.k + (16 * t + m) * w.kKS + (4 * u + q) * 8));
-#pragma unroll
-    for (int ti = 0; ti < KW / 16; ++ti)
-#pragma unroll
-      for (int tj = 0; tj <= ti; ++tj) s[ti * (ti + 1) / 2 + tj] = mfma_bf16(f[ti], f[tj], s[ti * (ti + 1) / 2 + tj]);
-  }
-}
 
 // 1 / |x| of 16 tokens from the diagonal of their Gram tile, in lanes 5 m
 // modulo 16 of every q (m / 4 == q); call with the lane's own tile.
@@ -191,42 +173,72 @@ __device__ __forceinline__ float unit_of(f32x4 diag, int m, int norm) {
   return norm ? 1.f / sqrtf(pick4(diag[0], diag[1], diag[2], diag[3], m & 3) + kDeltaEps) : 1.f;
 }
 
-// Writes A from the Gram tiles (G, b and rk are in LDS); rows from w on are 0
-// through b, the upper triangle and the diagonal are 0.
-template <int KW, int DK>
-__device__ __forceinline__ void write_A(WinLds<KW, DK> &w, int lane, const f32x4 (&s)[KW / 16 * (KW / 16 + 1) / 2]) {
-  const int m = lane & 15, q = lane >> 4;
+// Tiles of a window's Gram matrix are taken with the column as the token i of
+// a row of A or P and the rows as the tokens j <= i: lane (m, q) then holds four
+// neighbours j of row i = 16 ti + m.  Tile (tj, ti >= tj) is number
+// ti (ti + 1) / 2 + tj.
+constexpr int win_tiles(int KW) { return KW / 16 * (KW / 16 + 1) / 2; }
+
+// k_j . k_i from operands f (16 tokens each, one depth step of 32).
+template <int KW>
+__device__ __forceinline__ void gram_kk(const bf16x8 (&f)[KW / 16], f32x4 (&s)[win_tiles(KW)]) {
 #pragma unroll
   for (int ti = 0; ti < KW / 16; ++ti)
 #pragma unroll
-    for (int tj = 0; tj < KW / 16; ++tj) {
-      const int j = 16 * tj + m;
-      const double Gj = w.G[j];
-      const float rj = w.rk[j];
+    for (int tj = 0; tj <= ti; ++tj) s[ti * (ti + 1) / 2 + tj] = mfma_bf16(f[tj], f[ti], s[ti * (ti + 1) / 2 + tj]);
+}
+
+// 1 / |k| of the window's tokens from the diagonal tiles.
+template <int KW>
+__device__ __forceinline__ void write_rk(WinLds<KW> &w, int m, int q, const f32x4 (&kk)[win_tiles(KW)], int norm) {
+  if ((m >> 2) == q) {
+#pragma unroll
+    for (int t = 0; t < KW / 16; ++t) w.rk[16 * t + m] = unit_of(kk[t * (t + 3) / 2], m, norm);
+  }
+}
+
+// A from the Gram tiles (G, b and rk are in LDS), zero on and above the
+// diagonal and in the rows of tokens that are none (b = 0); `decay` gets
+// e^(G_i - G_j) / |k_j| of the same elements.
+template <int KW>
+__device__ __forceinline__ void write_A(WinLds<KW> &w, int m, int q, const f32x4 (&kk)[win_tiles(KW)], f32x4 (&decay)[win_tiles(KW)]) {
+#pragma unroll
+  for (int ti = 0; ti < KW / 16; ++ti) {
+    const int i = 16 * ti + m;
+    const double Gi = w.G[i];
+    const float bi = w.b[i] * w.rk[i];
+#pragma unroll
+    for (int tj = 0; tj <= ti; ++tj) {
+      const int n = ti * (ti + 1) / 2 + tj, j0 = 16 * tj + 4 * q;
+      const f32x4 rj = *reinterpret_cast<const f32x4 *>(w.rk + j0);
+      f32x4 a;
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const int i = 16 * ti + 4 * q + r;
-        float a = 0.f;
-        if (tj <= ti && j < i)
-          a = w.b[i] * w.rk[i] * rj * expf((float)(w.G[i] - Gj)) * s[tj <= ti ? ti * (ti + 1) / 2 + tj : 0][r];
-        w.A[i * w.kAS + j] = a;
+        decay[n][r] = exp2_d(Gi - w.G[j0 + r]) * rj[r];
+        a[r] = j0 + r < i ? bi * decay[n][r] * kk[n][r] : 0.f;
       }
+      *reinterpret_cast<f32x4 *>(w.A + i * w.kAS + j0) = a;
     }
+  }
 }
 
 // (I + A)^-1 of the 16x16 diagonal blocks, over them: lane l's row l % KW of
 // X (I + A) = I, whose column j is final once every later column is, and then
 // leaves the earlier ones.  120 dependent multiply-adds; the whole 32x32
 // triangle done this way would be 496, and its rows of A do not fit registers.
-template <int KW, int DK>
-__device__ __forceinline__ void invert_diag(WinLds<KW, DK> &w, int lane) {
-  const int i = lane & 15, blk = lane & (KW - 16);
+template <int KW>
+__device__ __forceinline__ void invert_diag(WinLds<KW> &w, int lane) {
+  int i = lane & 15;
+  asm("" : "+v"(i));  // (the first values of x are not worth 16 registers across a loop around this)
+  const int blk = lane & (KW - 16);
   float *A = w.A + blk * w.kAS + blk;
   float x[16];
 #pragma unroll
   for (int j = 0; j < 16; ++j) x[j] = j == i ? 1.f : 0.f;
 #pragma unroll
   for (int j = 15; j > 0; --j) {
+    // the rows of A of four steps at a time: all 40 reads ahead would spill
+    if (j % 4 == 3 && j < 15) asm volatile("" : : "v"(A) : "memory");
     const float xj = x[j];
 #pragma unroll
     for (int l0 = 0; l0 < j; l0 += 4) {
@@ -236,10 +248,9 @@ __device__ __forceinline__ void invert_diag(WinLds<KW, DK> &w, int lane) {
     }
   }
   wave_sync();
-  if (lane < KW) {
+  // lanes from KW on hold the same rows again and write the same values
 #pragma unroll
-    for (int j = 0; j < 16; j += 4) *reinterpret_cast<f32x4 *>(A + i * w.kAS + j) = f32x4{x[j], x[j + 1], x[j + 2], x[j + 3]};
-  }
+  for (int j = 0; j < 16; j += 4) *reinterpret_cast<f32x4 *>(A + i * w.kAS + j) = f32x4{x[j], x[j + 1], x[j + 2], x[j + 3]};
   wave_sync();
 }
 
@@ -266,8 +277,8 @@ __device__ __forceinline__ f32x4 block_row(const float *p, int stride, int m, in
 // Row 16 ti + m of T along the depth of KW tokens, after invert_diag: the block
 // below the diagonal is -T22 A21 T11, formed transposed so that its rows land
 // in their lanes.
-template <int KW, int DK>
-__device__ __forceinline__ void t_row(const WinLds<KW, DK> &w, int ti, int m, int q, float (&x)[KW / 4]) {
+template <int KW>
+__device__ __forceinline__ void t_row(const WinLds<KW> &w, int ti, int m, int q, float (&x)[KW / 4]) {
   const f32x4 d = block_row(w.A + 16 * ti * w.kAS + 16 * ti, w.kAS, m, q);
 #pragma unroll
   for (int r = 0; r < 4; ++r) x[4 * ti + r] = d[r];
@@ -285,14 +296,14 @@ __device__ __forceinline__ void t_row(const WinLds<KW, DK> &w, int ti, int m, in
   }
 }
 
-// Row m of M = P T along the depth, for a 16-row P: M2 = P2 T22,
-// M1 = (P1 - M2 A21) T11, transposed like t_row.
-template <int KW, int DK>
-__device__ __forceinline__ void m_row(const WinLds<KW, DK> &w, const float *P, int m, int q, float (&x)[KW / 4]) {
+// Row m of M = P T along the depth, for a 16-row P whose row m's values along
+// the depth are p: M2 = P2 T22, M1 = (P1 - M2 A21) T11, transposed like t_row.
+template <int KW>
+__device__ __forceinline__ void m_row(const WinLds<KW> &w, const f32x4 (&p)[KW / 16], int m, int q, float (&x)[KW / 4]) {
   const f32x4 z = {0.f, 0.f, 0.f, 0.f};
-  f32x4 p1 = block_row(P, w.kAS, m, q);
+  f32x4 p1 = p[0];
   if constexpr (KW == 32) {
-    const f32x4 m2 = mfma16_f32(block_col(w.A + 16 * w.kAS + 16, w.kAS, m, q), block_row(P + 16, w.kAS, m, q), z);
+    const f32x4 m2 = mfma16_f32(block_col(w.A + 16 * w.kAS + 16, w.kAS, m, q), p[1], z);
     const f32x4 a = mfma16_f32(block_col(w.A + 16 * w.kAS, w.kAS, m, q), m2, z);
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
@@ -303,17 +314,6 @@ __device__ __forceinline__ void m_row(const WinLds<KW, DK> &w, const float *P, i
   const f32x4 m1 = mfma16_f32(block_col(w.A, w.kAS, m, q), p1, z);
 #pragma unroll
   for (int r = 0; r < 4; ++r) x[r] = m1[r];
-}
-
-// A lane's values of row `row` of an LDS matrix along the depth of KW tokens.
-template <int KW>
-__device__ __forceinline__ void depth_row(const float *row, int q, float (&x)[KW / 4]) {
-#pragma unroll
-  for (int a = 0; a < KW / 16; ++a) {
-    const f32x4 v = *reinterpret_cast<const f32x4 *>(row + 16 * a + 4 * q);
-#pragma unroll
-    for (int r = 0; r < 4; ++r) x[4 * a + r] = v[r];
-  }
 }
 
 }  // namespace ssu

@@ -104,10 +104,10 @@ __global__ __launch_bounds__(64, 2) void delta_step_kernel(DCache c, DStep s, in
   constexpr int NQ = OT == kOutF32 ? 3 : 2, NS = ST == kF32 ? NQ : (ST == kF16 ? 2 : 1);
   constexpr int VS = RB * 16 + 8;
   typedef typename Tok<KW>::V TV;
-  __shared__ WinLds<KW, DK> w;
-  __shared__ __align__(16) float P[16 * (KW + 4)];
+  constexpr int KS = DK + 8;  // row strides in LDS: 8 values on, so 16 rows start in different banks
+  __shared__ WinLds<KW> w;
   __shared__ float rq[16];
-  __shared__ __align__(16) uint16_t vw[KW * VS];
+  __shared__ __align__(16) uint16_t kw[KW * KS], vw[KW * VS];
 
   const int64_t tile = xcd_tile(blockIdx.x, gridDim.x);
   if (tile >= nwaves) return;
@@ -157,7 +157,7 @@ __global__ __launch_bounds__(64, 2) void delta_step_kernel(DCache c, DStep s, in
       v = t < p ? ld16(at) : ld16(s.k + (int64_t)(e.bos + t - p) * s.k_stride + hk * DK + ch * 8);
       if (t >= p && first_k) st16(at, v);
     }
-    st16(w.k + t * w.kKS + ch * 8, v);
+    st16(kw + t * KS + ch * 8, v);
   }
 #pragma unroll
   for (int i = 0; i < (KW * RB * 2 + 63) / 64; ++i) {
@@ -192,58 +192,60 @@ __global__ __launch_bounds__(64, 2) void delta_step_kernel(DCache c, DStep s, in
       if (first) *at = gb;
     }
   }
-  const double G = scan_d<KW>((double)gb.x, lane);
+  const double G = scan_d<KW>((double)gb.x * kLog2e, lane);
   if (lane < KW) {
     w.G[lane] = G;
     w.b[lane] = gb.y;
   }
   wave_sync();
 
-  f32x4 kk[KW / 16 * (KW / 16 + 1) / 2], qk[KW / 16], qq = {0.f, 0.f, 0.f, 0.f};
-  gram_kk<KW, DK>(w, lane, kk);
+  // k . k and k . q over the window, and the units from their diagonals
+  f32x4 kk[win_tiles(KW)], qk[KW / 16], qq = {0.f, 0.f, 0.f, 0.f}, decay[win_tiles(KW)];
+#pragma unroll
+  for (int t = 0; t < win_tiles(KW); ++t) kk[t] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int t = 0; t < KW / 16; ++t) qk[t] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int u = 0; u < DK / 32; ++u) {
+    bf16x8 f[KW / 16];
+#pragma unroll
+    for (int t = 0; t < KW / 16; ++t) {
+      f[t] = __builtin_bit_cast(bf16x8, ld16(kw + (16 * t + m) * KS + (4 * u + q) * 8));
+      qk[t] = mfma_bf16(f[t], qn[u], qk[t]);
+    }
     qq = mfma_bf16(qn[u], qn[u], qq);
-#pragma unroll
-    for (int t = 0; t < KW / 16; ++t)
-      qk[t] = mfma_bf16(qn[u], __builtin_bit_cast(bf16x8, ld16(w.k + (16 * t + m) * w.kKS + (4 * u + q) * 8)), qk[t]);
+    gram_kk<KW>(f, kk);
   }
-  if ((m >> 2) == q) {
-#pragma unroll
-    for (int t = 0; t < KW / 16; ++t) w.rk[16 * t + m] = unit_of(kk[t * (t + 3) / 2], m, c.norm);
-    rq[m] = s.scale * unit_of(qq, m, c.norm);
-  }
+  write_rk<KW>(w, m, q, kk, c.norm);
+  if ((m >> 2) == q) rq[m] = s.scale * unit_of(qq, m, c.norm);
   wave_sync();
-  write_A<KW, DK>(w, lane, kk);
+  write_A<KW>(w, m, q, kk, decay);
+  // row m of P along the tokens
+  f32x4 P[KW / 16];
+  const int at = p + min(m, e.T - 1);
+  const double Gm = w.G[at];
+  const float rqm = m < e.T ? rq[m] : 0.f;
 #pragma unroll
   for (int t = 0; t < KW / 16; ++t) {
-    const int j = 16 * t + m;
-    const double Gj = w.G[j];
-    const float rj = w.rk[j];
+    const int j0 = 16 * t + 4 * q;
+    const f32x4 rj = *reinterpret_cast<const f32x4 *>(w.rk + j0);
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int i = 4 * q + r, at = p + i;
-      float v = 0.f;
-      if (i < e.T && j <= at) v = rq[i] * rj * expf((float)(w.G[at] - Gj)) * qk[t][r];
-      P[i * (KW + 4) + j] = v;
-    }
+    for (int r = 0; r < 4; ++r)
+      P[t][r] = j0 + r <= at ? rqm * rj[r] * exp2_d(Gm - w.G[j0 + r]) * qk[t][r] : 0.f;
   }
   wave_sync();
+  invert_diag<KW>(w, lane);
 
-  invert_diag<KW, DK>(w, lane);
-
-  // row m of M along the tokens: the weights of v and (with b e^G / |k|) of k
+  // row m of M: the weights of v and (with b e^G / |k|) of k
   float cv[E], ck[E];
-  m_row<KW, DK>(w, P, m, q, cv);
+  m_row<KW>(w, P, m, q, cv);
 #pragma unroll
   for (int a = 0; a < KW / 16; ++a)
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const int j = 16 * a + 4 * q + r;
       cv[4 * a + r] *= w.b[j];
-      ck[4 * a + r] = -cv[4 * a + r] * expf((float)w.G[j]) * w.rk[j];
+      ck[4 * a + r] = -cv[4 * a + r] * exp2_d(w.G[j]) * w.rk[j];
     }
   TV fv[NQ], fk[NQ];
   split<NQ>(cv, fv);
@@ -252,13 +254,13 @@ __global__ __launch_bounds__(64, 2) void delta_step_kernel(DCache c, DStep s, in
   // the queries, one column per new token
   bf16x8 fq[DK / 32][NQ];
   {
-    const float eq = m < e.T ? rq[m] * expf((float)w.G[p + m]) : 0.f;
+    const float eq = rqm * exp2_d(Gm);
     float y[DK / 4];
 #pragma unroll
     for (int t = 0; t < DK / 16; ++t) {
       f32x4 acc = {eq * bf2f(qd[t][0] & 0xFFFFu), eq * __uint_as_float(qd[t][0] & 0xFFFF0000u),
                    eq * bf2f(qd[t][1] & 0xFFFFu), eq * __uint_as_float(qd[t][1] & 0xFFFF0000u)};
-      acc = Tok<KW>::template exact<true>(Tok<KW>::load_tr(w.k, w.kKS, 16 * t, lane), fk, acc);
+      acc = Tok<KW>::template exact<true>(Tok<KW>::load_tr(kw, KS, 16 * t, lane), fk, acc);
 #pragma unroll
       for (int r = 0; r < 4; ++r) y[4 * t + r] = acc[r];
     }
@@ -310,11 +312,12 @@ template <int ST, int KW, int DK>
 __global__ __launch_bounds__(64, 2) void delta_flush_kernel(DCache c, const int32_t *slot_idx, const int32_t *num_fold,
                                                          int parts, int64_t nwaves) {
   constexpr int CH = dchunks(ST, DK), RB = kStepWaveChunks / CH, E = KW / 4, NT = KW / 16;
-  constexpr int NW = ST == kF32 ? 3 : 2, NS = ST == kF32 ? 3 : (ST == kF16 ? 2 : 1);
+  constexpr int NW = ST == kF32 ? 3 : 2, NS = ST == kBF16 ? 1 : 2;
   constexpr int VS = RB * 16 + 8;
   typedef typename Tok<KW>::V TV;
-  __shared__ WinLds<KW, DK> w;
-  __shared__ __align__(16) uint16_t vw[KW * VS];
+  constexpr int KS = DK + 8;
+  __shared__ WinLds<KW> w;
+  __shared__ __align__(16) uint16_t kw[KW * KS], vw[KW * VS];
 
   const int64_t tile = xcd_tile(blockIdx.x, gridDim.x);
   if (tile >= nwaves) return;
@@ -340,7 +343,7 @@ __global__ __launch_bounds__(64, 2) void delta_flush_kernel(DCache c, const int3
 #pragma unroll
   for (int i = 0; i < KW * (DK / 8) / 64; ++i) {
     const int t = (i * 64 + lane) / (DK / 8), ch = (i * 64 + lane) % (DK / 8);
-    st16(w.k + t * w.kKS + ch * 8,
+    st16(kw + t * KS + ch * 8,
          t < k ? ld16(ring_k + (ring_pos(ring, t, c.L) * DK + ch * 8) * 2) : u32x4{0, 0, 0, 0});
   }
 #pragma unroll
@@ -352,30 +355,35 @@ __global__ __launch_bounds__(64, 2) void delta_flush_kernel(DCache c, const int3
                                      : u32x4{0, 0, 0, 0});
   }
   const float2 gb = lane < k ? ring_g[ring_pos(ring, lane, c.L)] : float2{0.f, 0.f};
-  const double G = scan_d<KW>((double)gb.x, lane);
+  const double G = scan_d<KW>((double)gb.x * kLog2e, lane);
   if (lane < KW) {
     w.G[lane] = G;
     w.b[lane] = gb.y;
   }
   wave_sync();
   {
-    f32x4 kk[NT * (NT + 1) / 2];
-    gram_kk<KW, DK>(w, lane, kk);
-    if ((m >> 2) == q) {
+    f32x4 kk[win_tiles(KW)], decay[win_tiles(KW)];
 #pragma unroll
-      for (int t = 0; t < NT; ++t) w.rk[16 * t + m] = unit_of(kk[t * (t + 3) / 2], m, c.norm);
+    for (int t = 0; t < win_tiles(KW); ++t) kk[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int u = 0; u < DK / 32; ++u) {
+      bf16x8 f[NT];
+#pragma unroll
+      for (int t = 0; t < NT; ++t) f[t] = __builtin_bit_cast(bf16x8, ld16(kw + (16 * t + m) * KS + (4 * u + q) * 8));
+      gram_kk<KW>(f, kk);
     }
+    write_rk<KW>(w, m, q, kk, c.norm);
     wave_sync();
-    write_A<KW, DK>(w, lane, kk);
+    write_A<KW>(w, m, q, kk, decay);
   }
   wave_sync();
-  invert_diag<KW, DK>(w, lane);
+  invert_diag<KW>(w, lane);
 
   // T b (towards V) and W = T b e^G K^ as operands, rows = tokens
   TV ft[NT][NW], kt[DK / 16];
-  bf16x8 fw[NT][DK / 32][NW];
+  bf16x8 fw[NT][DK / 32][2];
 #pragma unroll
-  for (int t = 0; t < DK / 16; ++t) kt[t] = Tok<KW>::load_tr(w.k, w.kKS, 16 * t, lane);
+  for (int t = 0; t < DK / 16; ++t) kt[t] = Tok<KW>::load_tr(kw, KS, 16 * t, lane);
   float bj[E], ej[E];
 #pragma unroll
   for (int a = 0; a < NT; ++a)
@@ -383,12 +391,12 @@ __global__ __launch_bounds__(64, 2) void delta_flush_kernel(DCache c, const int3
     for (int r = 0; r < 4; ++r) {
       const int j = 16 * a + 4 * q + r;
       bj[4 * a + r] = w.b[j];
-      ej[4 * a + r] = -expf((float)w.G[j]) * w.rk[j];
+      ej[4 * a + r] = -exp2_d(w.G[j]) * w.rk[j];
     }
 #pragma unroll
   for (int ti = 0; ti < NT; ++ti) {
     float x[E], y[E];
-    t_row<KW, DK>(w, ti, m, q, x);
+    t_row<KW>(w, ti, m, q, x);
 #pragma unroll
     for (int i = 0; i < E; ++i) {
       x[i] *= bj[i];
@@ -406,18 +414,18 @@ __global__ __launch_bounds__(64, 2) void delta_flush_kernel(DCache c, const int3
 #pragma unroll
         for (int r = 0; r < 4; ++r) z[4 * a + r] = acc[r];
       }
-      split<NW>(z, fw[ti][ks]);
+      split<2>(z, fw[ti][ks]);
     }
   }
   const double Gw = w.G[KW - 1];
-  const float ew = expf((float)Gw);
+  const float ew = exp2_d(Gw);
   float fu[E];  // e^(G_w - G_i) / |k_i| of the lane's rows
 #pragma unroll
   for (int a = 0; a < NT; ++a)
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const int j = 16 * a + 4 * q + r;
-      fu[4 * a + r] = expf((float)(Gw - w.G[j])) * w.rk[j];
+      fu[4 * a + r] = exp2_d(Gw - w.G[j]) * w.rk[j];
     }
 
 #pragma unroll

@@ -1,14 +1,25 @@
 // The gated delta rule over whole sequences, in chunks of 32 tokens.
 //
-// Two kernels.  delta_chunk_kernel, one wave per (chunk, value head), all
-// chunks at once: what of a chunk does not need the state, T = (I + A)^-1 and
-// the masked decayed q . k products P, written as MFMA operands in bf16 parts.
-// delta_scan_kernel, one wave per (sequence, value head, 16 columns of
-// dim_v), the chunks in order: with the state's columns in registers,
+// Two kernels.  delta_chunk_kernel, all chunks at once: what of a chunk does
+// not need the state, T = (I + A)^-1 and the masked decayed q . k products P,
+// written as MFMA operands.  Then the chunks of a (sequence, value head) in
+// order, with the state's columns in registers:
 //   R = b (V - e^G K^ S^T),  U = T R,  O = scale e^G Q^ S^T + P U,
-//   S <- e^(G_w) S + (e^(G_w - G) U)^T K^.
-// The products towards the state carry 24 bits (three bf16 parts), those
-// towards the bf16 outputs 16.
+//   S <- e^(G_w) S + (e^(G_w - G) U)^T K^,
+// by delta_scan_kernel (a wave per 16 columns of dim_v) where there are many
+// such chains, by delta_chain_kernel (eight waves per 16 columns) where there
+// are few and each chunk's latency adds up.  Products with q, k and v take them
+// as they are (bf16); the state enters the products with k and q in two bf16
+// parts, U the update in three and the outputs in two, T R is fp32.
+//
+// What bounds them, at 8 sequences of 2048 to 4096 tokens with 64 heads of dim
+// 128: the chunk kernel takes 140 us (0.4 GB of records written), the scan 550:
+// its matrix instructions are busy for half of that (a third of them the fp32
+// product with T) and the rest of its vector instructions for the other half,
+// which four waves a SIMD do not overlap.  One sequence of 16384 tokens, 32
+// heads: 50 us of chunks, then 0.95 us for each of 512.
+#include <algorithm>
+
 #include "delta_device.cuh"
 
 namespace ssu {
@@ -41,250 +52,537 @@ __device__ __forceinline__ bool seq_rows(const DPrefill &p, int s, int &b0, int 
   return b0 >= 0 && b0 <= b1 && b1 <= p.rows;
 }
 
+// A wave takes a chunk of one key head: k . k and k . q once, then T and P of
+// `per` of the value heads that share it.
 template <int DK>
-__global__ __launch_bounds__(64, 2) void delta_chunk_kernel(DPrefill p) {
-  __shared__ WinLds<kChunk, DK> w;
-  __shared__ __align__(16) float P[kChunk * (kChunk + 4)];
-  __shared__ float rq[kChunk];
+__global__ __launch_bounds__(64, 3) void delta_chunk_kernel(DPrefill p, int per, int waves, int64_t ntiles) {
+  __shared__ WinLds<kChunk> w;
+  __shared__ __align__(16) float rq[kChunk];
   const int lane = threadIdx.x, m = lane & 15, q = lane >> 4;
-  const int h = blockIdx.x % p.Hv, slot = blockIdx.x / p.Hv, hk = h / p.hpg;
+  const int64_t tile = xcd_tile(blockIdx.x, gridDim.x);
+  if (tile >= ntiles) return;
+  const int part = (int)(tile % waves), hk = (int)(tile / waves % p.Hk), slot = (int)(tile / waves / p.Hk);
   const int seq = chunk_seq(p, slot, lane);
   int b0, b1;
   if (seq < 0 || !seq_rows(p, seq, b0, b1)) return;
   const int row0 = b0 + (slot - chunk_base(p, seq)) * kChunk, W = min(kChunk, b1 - row0);
   if (W <= 0) return;
 
-#pragma unroll
-  for (int i = 0; i < kChunk * (DK / 8) / 64; ++i) {
-    const int t = (i * 64 + lane) / (DK / 8), ch = (i * 64 + lane) % (DK / 8);
-    st16(w.k + t * w.kKS + ch * 8,
-         t < W ? ld16(p.k + (int64_t)(row0 + t) * p.k_stride + hk * DK + ch * 8) : u32x4{0, 0, 0, 0});
-  }
-  float2 gb = {0.f, 0.f};
-  if (lane < W) {
-    const int64_t o = (int64_t)(row0 + lane) * p.Hv + h;
-    gb = delta_gate(p.dt[o], p.beta[o], p.A[h], p.dt_bias[h], p.softplus, p.sigmoid);
-  }
-  const double G = scan_d<kChunk>((double)gb.x, lane);
-  if (lane < kChunk) {
-    w.G[lane] = G;
-    w.b[lane] = gb.y;
-  }
-  wave_sync();
+  const int h0 = hk * p.hpg + part * per, h1 = min(h0 + per, (hk + 1) * p.hpg);
+  const int64_t gate = (int64_t)(row0 + min(lane, W - 1)) * p.Hv;
+  float dt = p.dt[gate + h0], beta = p.beta[gate + h0], A = p.A[h0], bias = p.dt_bias[h0];
 
-  f32x4 kk[3], qk[3], qq[2];
-  gram_kk<kChunk, DK>(w, lane, kk);
+  f32x4 kk[3], qk[3], qq[2];  // tiles (tj, ti): tokens j = rows, i = columns
 #pragma unroll
-  for (int i = 0; i < 3; ++i) qk[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int i = 0; i < 3; ++i) kk[i] = qk[i] = f32x4{0.f, 0.f, 0.f, 0.f};
   qq[0] = qq[1] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-  for (int u = 0; u < DK / 32; ++u) {
-    bf16x8 f[2];
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      const int i = 16 * t + m;
-      u32x4 v = {0, 0, 0, 0};
-      if (i < W) v = ld16(p.q + (int64_t)(row0 + i) * p.q_stride + hk * DK + (4 * u + q) * 8);
-      f[t] = __builtin_bit_cast(bf16x8, v);
-      qq[t] = mfma_bf16(f[t], f[t], qq[t]);
-    }
-#pragma unroll
-    for (int tj = 0; tj < 2; ++tj) {
-      const bf16x8 kf = __builtin_bit_cast(bf16x8, ld16(w.k + (16 * tj + m) * w.kKS + (4 * u + q) * 8));
-#pragma unroll
-      for (int ti = tj; ti < 2; ++ti) qk[ti * (ti + 1) / 2 + tj] = mfma_bf16(f[ti], kf, qk[ti * (ti + 1) / 2 + tj]);
-    }
-  }
-  if ((m >> 2) == q) {
+  {
+    // tokens behind the sequence repeat its last one: their b is 0
+    const uint16_t *kr[2], *qr[2];
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-      w.rk[16 * t + m] = unit_of(kk[t * (t + 3) / 2], m, p.norm);
-      rq[16 * t + m] = p.scale * unit_of(qq[t], m, p.norm);
+      const int64_t row = row0 + min(16 * t + m, W - 1);
+      kr[t] = p.k + row * p.k_stride + hk * DK + q * 8;
+      qr[t] = p.q + row * p.q_stride + hk * DK + q * 8;
     }
-  }
-  wave_sync();
-  write_A<kChunk, DK>(w, lane, kk);
+    bf16x8 f[DK / 32][2], g[DK / 32][2];
 #pragma unroll
-  for (int ti = 0; ti < 2; ++ti)
+    for (int u = 0; u < DK / 32; ++u)
 #pragma unroll
-    for (int tj = 0; tj < 2; ++tj) {
-      const int j = 16 * tj + m;
-      const double Gj = w.G[j];
-      const float rj = w.rk[j];
+      for (int t = 0; t < 2; ++t) {
+        f[u][t] = __builtin_bit_cast(bf16x8, ld16(kr[t] + 32 * u));
+        g[u][t] = __builtin_bit_cast(bf16x8, ld16(qr[t] + 32 * u));
+      }
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int i = 16 * ti + 4 * q + r;
-        float v = 0.f;
-        if (tj <= ti && j <= i) v = rq[i] * rj * expf((float)(w.G[i] - Gj)) * qk[tj <= ti ? ti * (ti + 1) / 2 + tj : 0][r];
-        P[i * (kChunk + 4) + j] = v;
+    for (int u = 0; u < DK / 32; ++u) {
+      gram_kk<kChunk>(f[u], kk);
+#pragma unroll
+      for (int ti = 0; ti < 2; ++ti) {
+        qq[ti] = mfma_bf16(g[u][ti], g[u][ti], qq[ti]);
+#pragma unroll
+        for (int tj = 0; tj <= ti; ++tj) qk[ti + tj] = mfma_bf16(f[u][tj], g[u][ti], qk[ti + tj]);
       }
     }
-  wave_sync();
-  invert_diag<kChunk, DK>(w, lane);
-
-  uint8_t *rec = p.ws + ((int64_t)slot * p.Hv + h) * kRecBytes;
-#pragma unroll
-  for (int ti = 0; ti < 2; ++ti) {
-    float x[8];
-    bf16x8 f3[3], f2[2];
-    t_row<kChunk, DK>(w, ti, m, q, x);
-    split<3>(x, f3);
-#pragma unroll
-    for (int a = 0; a < 3; ++a) st16(rec + ((ti * 3 + a) * 64 + lane) * 16, __builtin_bit_cast(u32x4, f3[a]));
-    depth_row<kChunk>(P + (16 * ti + m) * (kChunk + 4), q, x);
-    split<2>(x, f2);
-#pragma unroll
-    for (int a = 0; a < 2; ++a) st16(rec + kRecT + ((ti * 2 + a) * 64 + lane) * 16, __builtin_bit_cast(u32x4, f2[a]));
   }
-  float *f = reinterpret_cast<float *>(rec + kRecT + kRecP);
-  if (lane < kChunk) {
-    const double Gw = w.G[kChunk - 1];
-    const float e = expf((float)G), rk = w.rk[lane];
-    f[lane] = gb.y;
-    f[32 + lane] = gb.y * e * rk;
-    f[64 + lane] = expf((float)(Gw - G)) * rk;
-    f[96 + lane] = rq[lane] * e;
-    if (lane == 0) f[128] = expf((float)Gw);
+  write_rk<kChunk>(w, m, q, kk, p.norm);
+  if ((m >> 2) == q) {
+#pragma unroll
+    for (int t = 0; t < 2; ++t) rq[16 * t + m] = p.scale * unit_of(qq[t], m, p.norm);
+  }
+
+  for (int h = h0; h < h1; ++h) {
+    float2 gb = delta_gate(dt, beta, A, bias, p.softplus, p.sigmoid);
+    if (lane >= W) gb = float2{0.f, 0.f};
+    const int next = min(h + 1, h1 - 1);
+    dt = p.dt[gate + next];
+    beta = p.beta[gate + next];
+    A = p.A[next];
+    bias = p.dt_bias[next];
+    const double G = scan_d<kChunk>((double)gb.x * kLog2e, lane);
+    wave_sync();
+    if (lane < kChunk) {
+      w.G[lane] = G;
+      w.b[lane] = gb.y;
+    }
+    wave_sync();
+    f32x4 decay[3];
+    write_A<kChunk>(w, m, q, kk, decay);
+    uint8_t *rec = p.ws + ((int64_t)slot * p.Hv + h) * kRecBytes;
+#pragma unroll
+    for (int ti = 0; ti < 2; ++ti) {
+      const int i = 16 * ti + m;
+      const float r = rq[i];
+      float x[8];
+#pragma unroll
+      for (int a = 0; a < 2; ++a)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          x[4 * a + e] = a <= ti && 16 * a + 4 * q + e <= i ? r * decay[a <= ti ? ti + a : 0][e] * qk[a <= ti ? ti + a : 0][e] : 0.f;
+      bf16x8 f[2];
+      split<2>(x, f);
+#pragma unroll
+      for (int a = 0; a < 2; ++a) {
+        const u32x4 v = __builtin_bit_cast(u32x4, f[a]);
+        if (ti == 0)
+          st8(rec + kRecT + (a * 64 + lane) * 8, u32x2{v[0], v[1]});
+        else
+          st16(rec + kRecT + 2 * 64 * 8 + (a * 64 + lane) * 16, v);
+      }
+    }
+    wave_sync();
+    invert_diag<kChunk>(w, lane);
+#pragma unroll
+    for (int ti = 0; ti < 2; ++ti) {
+      float x[8];
+      t_row<kChunk>(w, ti, m, q, x);
+#pragma unroll
+      for (int a = 0; a <= ti; ++a)
+        st16(rec + ((ti + a) * 64 + lane) * 16, __builtin_bit_cast(u32x4, f32x4{x[4 * a], x[4 * a + 1], x[4 * a + 2], x[4 * a + 3]}));
+    }
+    float *f = reinterpret_cast<float *>(rec + kRecT + kRecP);
+    if (lane < kChunk) {
+      const double Gw = w.G[kChunk - 1];
+      const float e = exp2_d(G), rk = w.rk[lane];
+      f[lane] = gb.y;
+      f[32 + lane] = gb.y * e * rk;
+      f[64 + lane] = exp2_d(Gw - G) * rk;
+      f[96 + lane] = rq[lane] * e;
+      if (lane == 0) f[128] = exp2_d(Gw);
+    }
   }
 }
 
-constexpr int kScanWaves = 4;
+// 16-byte pieces of a chunk that NT threads stage, per thread.
+constexpr int pieces(int n, int NT) { return (n + NT - 1) / NT; }
 
-template <int OT, int DK>
-__global__ __launch_bounds__(kScanWaves * 64) void delta_scan_kernel(DPrefill p, int groups) {
-  constexpr int KS = DK + 8, VS = kScanWaves * 16 + 8, NT = DK / 16, NK = DK / 32;
-  __shared__ __align__(16) uint16_t lk[kChunk * KS], lq[kChunk * KS], lv[kChunk * VS];
+// What the waves of a chain share of a chunk.
+template <int DK, int COLS>
+struct Chunk {
+  static constexpr int KS = DK + 8, VS = COLS + 8;  // row strides: 16 rows start in different banks
+  __align__(16) uint16_t k[kChunk * KS], q[kChunk * KS], v[kChunk * VS];
+  __align__(16) uint8_t rec[kRecBytes];
+  __device__ __forceinline__ const float *factors() const { return reinterpret_cast<const float *>(rec + kRecT + kRecP); }
+};
+
+// One sequence's chunks of a head's columns c0 .. c0 + COLS - 1.
+struct Chain {
+  int b0, b1, h, c0, chunks;
+};
+
+// A chunk on its way from memory to LDS through the registers of NT threads.
+// Every load is unconditional, so that the waits of a loop around them count
+// exactly: behind the sequence's end (and the last chunk) they repeat its last
+// row (and chunk), whose gates in the record are 0, and columns behind dim_v
+// repeat the first ones.
+template <int DK, int COLS, int NT>
+struct Stage {
+  typedef Chunk<DK, COLS> Buf;
+  static constexpr int PK = pieces(kChunk * DK / 8, NT), PV = pieces(kChunk * COLS / 8, NT), PR = pieces(kRecBytes / 16, NT);
+  u32x4 k[PK], q[PK], v[PV], r[PR];
+
+  __device__ __forceinline__ void fetch(const DPrefill &p, const Chain &n, const uint8_t *rec0, int c, int tid) {
+    c = min(c, n.chunks - 1);
+    const int last = min(kChunk, n.b1 - n.b0 - c * kChunk) - 1;
+    // uniform bases and 32-bit byte offsets of the lanes
+    const int64_t row = n.b0 + c * kChunk;
+    const int hk = n.h / p.hpg, ks = (int)p.k_stride * 2, qs = (int)p.q_stride * 2, vs = (int)p.v_stride * 2;
+    const char *kc = reinterpret_cast<const char *>(p.k + row * p.k_stride + hk * DK);
+    const char *qc = reinterpret_cast<const char *>(p.q + row * p.q_stride + hk * DK);
+    const char *vc = reinterpret_cast<const char *>(p.v + row * p.v_stride + n.h * p.dv + n.c0);
+    const uint8_t *rec = rec0 + (int64_t)c * p.Hv * kRecBytes;
+#pragma unroll
+    for (int i = 0; i < PK; ++i) {
+      const int at = i * NT + tid, t = min(at / (DK / 8), last), ch = at % (DK / 8);
+      k[i] = ld16(kc + (uint32_t)(t * ks + ch * 16));
+      q[i] = ld16(qc + (uint32_t)(t * qs + ch * 16));
+    }
+#pragma unroll
+    for (int i = 0; i < PV; ++i) {
+      const int at = i * NT + tid, t = min(at / (COLS / 8), last), ch = at % (COLS / 8);
+      v[i] = ld16(vc + (uint32_t)(t * vs + (n.c0 + ch * 8 < p.dv ? ch * 16 : 0)));
+    }
+#pragma unroll
+    for (int i = 0; i < PR; ++i) r[i] = ld16(rec + (uint32_t)(min(i * NT + tid, kRecBytes / 16 - 1) * 16));
+  }
+
+  // (a thread without a piece of its own writes the last one again)
+  __device__ __forceinline__ void store(Buf &o, int tid) const {
+#pragma unroll
+    for (int i = 0; i < PK; ++i) {
+      const int at = min(i * NT + tid, kChunk * DK / 8 - 1), t = at / (DK / 8), ch = at % (DK / 8);
+      st16(o.k + t * Buf::KS + ch * 8, k[i]);
+      st16(o.q + t * Buf::KS + ch * 8, q[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < PV; ++i) {
+      const int at = min(i * NT + tid, kChunk * COLS / 8 - 1), t = at / (COLS / 8), ch = at % (COLS / 8);
+      st16(o.v + t * Buf::VS + ch * 8, v[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < PR; ++i) st16(o.rec + min(i * NT + tid, kRecBytes / 16 - 1) * 16, r[i]);
+  }
+};
+
+// Lane (m, q) of a wave holds column m of a block of 16 columns of dim_v; of
+// the state the rows n = n0 + 32 i + 8 q + 4 a + r in S[i][a][r], of the tokens
+// the rows 16 ti + 4 q + r.
+
+// x += K S^T (rows = tokens), o += Q S^T (transposed: columns = tokens), over
+// the wave's rows of the state; S in 16 of its 24 bits, which moves a state by
+// 2^-20.6 of its norm in the mean (two bf16 parts, each rounded to nearest).
+template <int DK, int COLS, int NK>
+__device__ __forceinline__ void state_products(const Chunk<DK, COLS> &in, const f32x4 (&S)[NK][2], int n0, int m, int q,
+                                               f32x4 (&x)[2], f32x4 (&o)[2]) {
+#pragma unroll
+  for (int i = 0; i < NK; ++i) {
+    bf16x8 fs[2], kf[2], qf[2];
+    float y[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y[e] = S[i][e / 4][e % 4];
+    split<2>(y, fs);
+#pragma unroll
+    for (int ti = 0; ti < 2; ++ti) {
+      const int at = (16 * ti + m) * in.KS + n0 + 32 * i + 8 * q;
+      kf[ti] = __builtin_bit_cast(bf16x8, ld16(in.k + at));
+      qf[ti] = __builtin_bit_cast(bf16x8, ld16(in.q + at));
+    }
+#pragma unroll
+    for (int a = 1; a >= 0; --a)
+#pragma unroll
+      for (int ti = 0; ti < 2; ++ti) {
+        x[ti] = mfma_bf16(kf[ti], fs[a], x[ti]);
+        o[ti] = mfma_bf16(fs[a], qf[ti], o[ti]);
+      }
+  }
+}
+
+// U = T (b V - (b e^G / |k|) K S^T), T and the product in fp32.
+template <int DK, int COLS>
+__device__ __forceinline__ void residuals(const Chunk<DK, COLS> &in, int block, int lane, const f32x4 (&x)[2], f32x4 (&U)[2]) {
+  const int m = lane & 15, q = lane >> 4;
+  const float *fac = in.factors();
+  const f32x4 *T = reinterpret_cast<const f32x4 *>(in.rec) + lane;
+  const f32x4 t00 = T[0], t10 = T[64], t11 = T[128];
+  f32x4 R[2];
+#pragma unroll
+  for (int ti = 0; ti < 2; ++ti) {
+    const f32x4 b = *reinterpret_cast<const f32x4 *>(fac + 16 * ti + 4 * q);
+    const f32x4 be = *reinterpret_cast<const f32x4 *>(fac + 32 + 16 * ti + 4 * q);
+    const s16x4 v = lds_tr4(in.v + (16 * ti + 4 * q + (m >> 2)) * in.VS + block * 16 + 4 * (m & 3));
+#pragma unroll
+    for (int r = 0; r < 4; ++r) R[ti][r] = fmaf(-be[r], x[ti][r], b[r] * bf2f((uint16_t)v[r]));
+    U[ti] = f32x4{0.f, 0.f, 0.f, 0.f};
+  }
+  f32x4 u = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    U[0] = mfma_f32(t00[i], R[0][i], U[0]);
+    U[1] = mfma_f32(t10[i], R[0][i], U[1]);
+    u = mfma_f32(t11[i], R[1][i], u);
+  }
+  U[1] += u;
+}
+
+// S <- e^(G_w) S + (e^(G_w - G) U / |k|)^T K, the product from 24 bits of U.
+template <int DK, int COLS, int NK>
+__device__ __forceinline__ void update_state(const Chunk<DK, COLS> &in, f32x4 (&S)[NK][2], int n0, int lane, const f32x4 (&U)[2]) {
+  const int m = lane & 15, q = lane >> 4;
+  const float *fac = in.factors();
+  float y[8];
+#pragma unroll
+  for (int ti = 0; ti < 2; ++ti) {
+    const f32x4 e = *reinterpret_cast<const f32x4 *>(fac + 64 + 16 * ti + 4 * q);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) y[4 * ti + r] = U[ti][r] * e[r];
+  }
+  bf16x8 f[3];
+  split<3>(y, f);
+  const float ew = fac[128];
+#pragma unroll
+  for (int i = 0; i < NK; ++i)
+#pragma unroll
+    for (int a = 0; a < 2; ++a) {
+      // row m = 4 j + r of the tile is n = 32 i + 8 j + 4 a + r
+      const uint16_t *at = in.k + (4 * q + (m >> 2)) * in.KS + n0 + 32 * i + 8 * (m & 3) + 4 * a;
+      struct { s16x4 lo, hi; } kt = {lds_tr4(at), lds_tr4(at + 16 * in.KS)};
+      S[i][a] = Tok<32>::exact<true>(__builtin_bit_cast(bf16x8, kt), f, scale4(S[i][a], ew));
+    }
+}
+
+// Outputs of tokens 16 ti .. of a chunk: (scale e^G / |q|) Q S^T + P U, from o =
+// Q S^T.  Rows behind the sequence, columns behind dim_v and waves that have
+// nothing to write (!on) go past the buffer's end, where the hardware drops
+// them: a branch around the store would cost the loop its exact waits.
+template <int OT, int DK, int COLS>
+__device__ __forceinline__ void write_outputs(const DPrefill &p, const Chain &n, const Chunk<DK, COLS> &in, int c, int ti, int col,
+                                              bool on, int lane, const bf16x8 (&fu)[2], f32x4 o) {
+  const int m = lane & 15, q = lane >> 4;
+  constexpr int kOut = OT == kOutF32 ? 4 : 2;
+  const int row0 = n.b0 + c * kChunk, rows = min(kChunk, n.b1 - row0), row_bytes = p.Hv * p.dv * kOut;
+  const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(static_cast<uint8_t *>(p.out) + (int64_t)row0 * row_bytes, 0,
+                                                      rows * row_bytes, 0x00020000);
+  bf16x8 f[2];
+#pragma unroll
+  for (int a = 0; a < 2; ++a) {
+    u32x4 v = {0, 0, 0, 0};
+    if (ti == 0) {
+      const u32x2 lo = ld8(in.rec + kRecT + (a * 64 + lane) * 8);
+      v[0] = lo[0];
+      v[1] = lo[1];
+    } else {
+      v = ld16(in.rec + kRecT + 2 * 64 * 8 + (a * 64 + lane) * 16);
+    }
+    f[a] = __builtin_bit_cast(bf16x8, v);
+  }
+  const int t = 16 * ti + m;
+  o = mfma_parts(fu, f, scale4(o, in.factors()[96 + t]));
+  const int at = t < rows && col < p.dv && on ? t * row_bytes + (n.h * p.dv + col + 4 * q) * kOut : 0x7FFFFFF0;
+  if constexpr (OT == kOutF32)
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, o), rsrc, at, 0, 0);
+  else
+    __builtin_amdgcn_raw_buffer_store_b64(u32x2{pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3])}, rsrc, at, 0, 0);
+}
+
+__device__ __forceinline__ void split_u(const f32x4 (&U)[2], bf16x8 (&fu)[2]) {
+  const float y[8] = {U[0][0], U[0][1], U[0][2], U[0][3], U[1][0], U[1][1], U[1][2], U[1][3]};
+  split<2>(y, fu);
+}
+
+// The lane's rows of the state from and to the fp32 states of a sequence.
+template <int NK>
+__device__ __forceinline__ void load_state(const float *h0, int64_t at, bool on, f32x4 (&S)[NK][2]) {
+#pragma unroll
+  for (int i = 0; i < NK; ++i)
+#pragma unroll
+    for (int a = 0; a < 2; ++a)
+      S[i][a] = on && h0 ? *reinterpret_cast<const f32x4 *>(h0 + at + 32 * i + 4 * a) : f32x4{0.f, 0.f, 0.f, 0.f};
+  // The states have arrived before the loop that follows: a load of theirs
+  // still in flight there would make every iteration wait for all of its own.
+#pragma unroll
+  for (int i = 0; i < NK; ++i) asm volatile("" : "+v"(S[i][0]), "+v"(S[i][1]));
+}
+template <int NK>
+__device__ __forceinline__ void store_state(float *h1, int64_t at, bool on, const f32x4 (&S)[NK][2]) {
+  if (!on || !h1) return;
+#pragma unroll
+  for (int i = 0; i < NK; ++i)
+#pragma unroll
+    for (int a = 0; a < 2; ++a) *reinterpret_cast<f32x4 *>(h1 + at + 32 * i + 4 * a) = S[i][a];
+}
+
+// Sequence, head and columns of a workgroup; false where the sequence is not
+// what it has to be (the first workgroup of its first head says so).  An XCD
+// takes neighbours, the column groups of a head and the heads of a key head,
+// which read the same chunks: with them spread over the XCDs 32 chains of
+// 16384 tokens took 687 us, as every L2 fetched them all.
+template <int COLS>
+__device__ __forceinline__ bool chain_of(const DPrefill &p, int groups, Chain &n, int &seq) {
+  const int tile = (int)xcd_tile(blockIdx.x, gridDim.x);
+  if (tile >= p.n * p.Hv * groups) return false;
+  const int cg = tile % groups;
+  n.h = tile / groups % p.Hv;
+  seq = tile / groups / p.Hv;
+  n.c0 = cg * COLS;
+  const bool ok = seq_rows(p, seq, n.b0, n.b1);
+  if (!ok && p.status && cg == 0 && n.h == 0 && threadIdx.x == 0) atomicOr(p.status, SSU_STATUS_BAD_SEQLEN);
+  n.chunks = (n.b1 - n.b0 + kChunk - 1) / kChunk;
+  return ok;
+}
+
+// NC blocks of 16 columns of one chain, a wave each.  While chunk c is worked
+// on, chunk c + 1 goes to the other LDS buffer and chunk c + 2 is on its way to
+// registers, with one barrier a chunk: behind it everyone has read chunk c - 1.
+// LDS reads bound a lone workgroup and its waves wait at the same places, so
+// two workgroups share a CU (8 sequences of 2048 to 4096 tokens, 64 heads of
+// dim 128: 800 us with one and three buffers, 691 with two).
+template <int OT, int DK, int NC>
+__global__ __launch_bounds__(NC * 64, 2) void delta_scan_kernel(DPrefill p, int groups) {
+  constexpr int COLS = NC * 16, NK = DK / 32;
+  __shared__ Chunk<DK, COLS> buf[2];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, m = lane & 15, q = lane >> 4;
-  const int cg = blockIdx.x % groups, h = blockIdx.x / groups % p.Hv, seq = blockIdx.x / groups / p.Hv, hk = h / p.hpg;
-  int b0, b1;
-  if (!seq_rows(p, seq, b0, b1)) {
-    if (p.status && cg == 0 && h == 0 && tid == 0) atomicOr(p.status, SSU_STATUS_BAD_SEQLEN);
-    return;
-  }
-  const int c0 = cg * kScanWaves * 16, col = c0 + wave * 16;  // first column of the group, of the wave
-  const bool on = col < p.dv;
-
-  f32x4 S[NT];  // rows n = 16 t + 4 q + r of the column m
-  const int64_t state = (((int64_t)seq * p.Hv + h) * p.dv + col + m) * DK + 4 * q;
+  Chain n;
+  int seq;
+  if (!chain_of<COLS>(p, groups, n, seq)) return;
+  const int col = n.c0 + wave * 16;
+  f32x4 S[NK][2];
+  const int64_t state = (((int64_t)seq * p.Hv + n.h) * p.dv + col + m) * DK + 8 * q;
+  load_state(p.h0, state, col < p.dv, S);
+  if (n.chunks > 0) {
+    const uint8_t *rec0 = p.ws + ((int64_t)chunk_base(p, seq) * p.Hv + n.h) * kRecBytes;
+    Stage<DK, COLS, NC * 64> st;
+    st.fetch(p, n, rec0, 0, tid);
+    st.store(buf[0], tid);
+    st.fetch(p, n, rec0, 1, tid);
+    for (int c = 0; c < n.chunks; ++c) {
+      const Chunk<DK, COLS> &in = buf[c & 1];
+      __syncthreads();
+      st.store(buf[(c + 1) & 1], tid);
+      st.fetch(p, n, rec0, c + 2, tid);
+      f32x4 x[2], o[2], U[2];
+      x[0] = x[1] = o[0] = o[1] = f32x4{0.f, 0.f, 0.f, 0.f};
+      state_products(in, S, 0, m, q, x, o);
+      residuals(in, wave, lane, x, U);
+      update_state(in, S, 0, lane, U);
+      bf16x8 fu[2];
+      split_u(U, fu);
 #pragma unroll
-  for (int t = 0; t < NT; ++t)
-    S[t] = on && p.h0 ? *reinterpret_cast<const f32x4 *>(p.h0 + state + 16 * t) : f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int ti = 0; ti < 2; ++ti) write_outputs<OT>(p, n, in, c, ti, col, true, lane, fu, o[ti]);
+    }
+  }
+  store_state(p.h1, state, col < p.dv, S);
+}
 
-  const int first = chunk_base(p, seq);
-  for (int c = 0, row0 = b0; row0 < b1; ++c, row0 += kChunk) {
-    const int W = min(kChunk, b1 - row0);
-    __syncthreads();  // the chunk before has been read
-    for (int i = tid; i < kChunk * (DK / 8); i += kScanWaves * 64) {
-      const int t = i / (DK / 8), ch = i % (DK / 8);
-      u32x4 a = {0, 0, 0, 0}, b = {0, 0, 0, 0};
-      if (t < W) {
-        a = ld16(p.k + (int64_t)(row0 + t) * p.k_stride + hk * DK + ch * 8);
-        b = ld16(p.q + (int64_t)(row0 + t) * p.q_stride + hk * DK + ch * 8);
+// One block of 16 columns of one chain, for few chains, where a chunk's latency
+// is all that counts: DK / 32 waves hold 32 rows n of the state each and sum
+// their products with k through LDS; four more waves keep everything else off
+// the chain, the chunks' way into LDS and the outputs, which they form two
+// chunks behind.  One barrier a chunk (where the sums are exchanged); between
+// those of chunks c - 1 and c the chain reads chunks c - 1 and c, the helpers
+// write chunk c + 1 and read c - 2: four buffers.
+template <int OT, int DK>
+__global__ __launch_bounds__((DK / 32 + 4) * 64, 1) void delta_chain_kernel(DPrefill p, int groups) {
+  constexpr int NS = DK / 32, NH = 4;
+  __shared__ Chunk<DK, 16> buf[4];
+  __shared__ f32x4 red_x[2][NS][2][64], red_o[3][NS][2][64], shared_u[2][2][64];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, m = lane & 15, q = lane >> 4;
+  Chain n;
+  int seq;
+  if (!chain_of<16>(p, groups, n, seq)) return;
+  const uint8_t *rec0 = p.ws + ((int64_t)chunk_base(p, seq) * p.Hv + n.h) * kRecBytes;
+  if (wave < NS) {
+    f32x4 S[1][2];
+    const int64_t state = (((int64_t)seq * p.Hv + n.h) * p.dv + n.c0 + m) * DK + wave * 32 + 8 * q;
+    load_state(p.h0, state, true, S);
+    if (n.chunks > 0) {
+      __builtin_amdgcn_s_setprio(2);
+      __syncthreads();
+      for (int c = 0; c < n.chunks; ++c) {
+        const Chunk<DK, 16> &in = buf[c & 3];
+        f32x4 x[2], o[2], U[2];
+        x[0] = x[1] = o[0] = o[1] = f32x4{0.f, 0.f, 0.f, 0.f};
+        state_products(in, S, wave * 32, m, q, x, o);
+#pragma unroll
+        for (int ti = 0; ti < 2; ++ti) {
+          red_x[c & 1][wave][ti][lane] = x[ti];
+          red_o[c % 3][wave][ti][lane] = o[ti];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int ti = 0; ti < 2; ++ti) {
+          x[ti] = red_x[c & 1][0][ti][lane];
+#pragma unroll
+          for (int w = 1; w < NS; ++w) x[ti] += red_x[c & 1][w][ti][lane];
+        }
+        residuals(in, 0, lane, x, U);
+        if (wave == 0) {
+          shared_u[c & 1][0][lane] = U[0];
+          shared_u[c & 1][1][lane] = U[1];
+        }
+        update_state(in, S, wave * 32, lane, U);
       }
-      st16(lk + t * KS + ch * 8, a);
-      st16(lq + t * KS + ch * 8, b);
+      __syncthreads();
     }
-    for (int i = tid; i < kChunk * (kScanWaves * 2); i += kScanWaves * 64) {
-      const int t = i / (kScanWaves * 2), ch = i % (kScanWaves * 2);
-      u32x4 a = {0, 0, 0, 0};
-      if (t < W && c0 + ch * 8 < p.dv) a = ld16(p.v + (int64_t)(row0 + t) * p.v_stride + h * p.dv + c0 + ch * 8);
-      st16(lv + t * VS + ch * 8, a);
-    }
+    store_state(p.h1, state, true, S);
+  } else if (n.chunks > 0) {
+    const int ht = tid - NS * 64, hw = wave - NS;
+    // outputs of tokens 16 (hw % 2) .. of chunk c, by helpers 0 and 1
+    auto outputs = [&](int c) {
+      f32x4 o = red_o[c % 3][0][hw & 1][lane];
+#pragma unroll
+      for (int w = 1; w < NS; ++w) o += red_o[c % 3][w][hw & 1][lane];
+      const f32x4 U[2] = {shared_u[c & 1][0][lane], shared_u[c & 1][1][lane]};
+      bf16x8 fu[2];
+      split_u(U, fu);
+      write_outputs<OT>(p, n, buf[c & 3], c, hw & 1, n.c0, hw < 2, lane, fu, o);
+    };
+    // chunk c + 2 is fetched while c + 1 is stored: two register sets, so that
+    // a chunk has more than an iteration to arrive
+    Stage<DK, 16, NH * 64> st[2];
+    st[0].fetch(p, n, rec0, 0, ht);
+    st[1].fetch(p, n, rec0, 1, ht);
+    st[0].store(buf[0], ht);
     __syncthreads();
-    if (!on) continue;
-
-    const uint8_t *rec = p.ws + ((int64_t)(first + c) * p.Hv + h) * kRecBytes;
-    const float *fac = reinterpret_cast<const float *>(rec + kRecT + kRecP);
-
-    bf16x8 fs[NK][3];
-#pragma unroll
-    for (int ks = 0; ks < NK; ++ks) {
-      float x[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = S[2 * ks + i / 4][i % 4];
-      split<3>(x, fs[ks]);
+    auto serve = [&](int c, Stage<DK, 16, NH * 64> &has, Stage<DK, 16, NH * 64> &free) {
+      free.fetch(p, n, rec0, c + 2, ht);
+      has.store(buf[(c + 1) & 3], ht);
+      if (c >= 2) outputs(c - 2);
+      __syncthreads();
+    };
+    for (int c = 0; c < n.chunks; c += 2) {
+      serve(c, st[1], st[0]);
+      if (c + 1 >= n.chunks) break;
+      serve(c + 1, st[0], st[1]);
     }
-
-    // R = b V - (b e^G / |k|) K S^T, and O = (scale e^G / |q|) Q S^T transposed
-    f32x4 o[2];
-    float R[8];
-#pragma unroll
-    for (int ti = 0; ti < 2; ++ti) {
-      f32x4 x = {0.f, 0.f, 0.f, 0.f}, y = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int ks = 0; ks < NK; ++ks) {
-        const int at = (16 * ti + m) * KS + 32 * ks + 4 * q;
-        struct { u32x2 a, b; } fk = {ld8(lk + at), ld8(lk + at + 16)}, fq = {ld8(lq + at), ld8(lq + at + 16)};
-        const bf16x8 k1[1] = {__builtin_bit_cast(bf16x8, fk)}, q1[1] = {__builtin_bit_cast(bf16x8, fq)};
-        x = mfma_parts(k1, fs[ks], x);
-        y = mfma_bf16(fs[ks][1], q1[0], y);
-        y = mfma_bf16(fs[ks][0], q1[0], y);
-      }
-      const f32x4 b = *reinterpret_cast<const f32x4 *>(fac + 16 * ti + 4 * q);
-      const f32x4 be = *reinterpret_cast<const f32x4 *>(fac + 32 + 16 * ti + 4 * q);
-      const s16x4 v = lds_tr4(lv + (16 * ti + 4 * q + (m >> 2)) * VS + wave * 16 + 4 * (m & 3));
-#pragma unroll
-      for (int r = 0; r < 4; ++r) R[4 * ti + r] = b[r] * bf2f((uint16_t)v[r]) - be[r] * x[r];
-      o[ti] = scale4(y, fac[96 + 16 * ti + m]);
-    }
-    bf16x8 fr[3];
-    split<3>(R, fr);
-    float U[8], Ue[8];
-#pragma unroll
-    for (int ti = 0; ti < 2; ++ti) {
-      bf16x8 T[3];
-#pragma unroll
-      for (int a = 0; a < 3; ++a) T[a] = __builtin_bit_cast(bf16x8, ld16(rec + ((ti * 3 + a) * 64 + lane) * 16));
-      const f32x4 u = mfma_parts(T, fr, f32x4{0.f, 0.f, 0.f, 0.f});
-      const f32x4 e = *reinterpret_cast<const f32x4 *>(fac + 64 + 16 * ti + 4 * q);
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        U[4 * ti + r] = u[r];
-        Ue[4 * ti + r] = u[r] * e[r];
-      }
-    }
-    bf16x8 fu[2], fe[3];
-    split<2>(U, fu);
-    split<3>(Ue, fe);
-#pragma unroll
-    for (int ti = 0; ti < 2; ++ti) {
-      bf16x8 f[2];
-#pragma unroll
-      for (int a = 0; a < 2; ++a) f[a] = __builtin_bit_cast(bf16x8, ld16(rec + kRecT + ((ti * 2 + a) * 64 + lane) * 16));
-      o[ti] = mfma_parts(fu, f, o[ti]);
-      if (16 * ti + m < W) {
-        const int64_t at = ((int64_t)(row0 + 16 * ti + m) * p.Hv + h) * p.dv + col + 4 * q;
-        if constexpr (OT == kOutF32)
-          st16(static_cast<float *>(p.out) + at, __builtin_bit_cast(u32x4, o[ti]));
-        else
-          st8(static_cast<uint16_t *>(p.out) + at, u32x2{pack_bf16(o[ti][0], o[ti][1]), pack_bf16(o[ti][2], o[ti][3])});
-      }
-    }
-    const float ew = fac[128];
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      S[t] = Tok<32>::exact<true>(Tok<32>::load_tr(lk, KS, 16 * t, lane), fe, scale4(S[t], ew));
-    }
+    if (n.chunks >= 2) outputs(n.chunks - 2);
+    __syncthreads();
+    outputs(n.chunks - 1);
   }
-  if (on && p.h1) {
-#pragma unroll
-    for (int t = 0; t < NT; ++t) *reinterpret_cast<f32x4 *>(p.h1 + state + 16 * t) = S[t];
-  }
+}
+
+template <int DK, int NC>
+hipError_t scan_launch(const DPrefill &p, int out_type, hipStream_t st) {
+  const int groups = (p.dv + NC * 16 - 1) / (NC * 16);
+  const dim3 grid(xcd_grid((int64_t)p.n * p.Hv * groups)), block(NC * 64);
+  if (out_type == kOutF32)
+    delta_scan_kernel<kOutF32, DK, NC><<<grid, block, 0, st>>>(p, groups);
+  else
+    delta_scan_kernel<kOutBF16, DK, NC><<<grid, block, 0, st>>>(p, groups);
+  return hipGetLastError();
+}
+
+template <int DK>
+hipError_t chain_launch(const DPrefill &p, int out_type, hipStream_t st) {
+  const int groups = p.dv / 16;
+  const dim3 grid(xcd_grid((int64_t)p.n * p.Hv * groups)), block((DK / 32 + 4) * 64);
+  if (out_type == kOutF32)
+    delta_chain_kernel<kOutF32, DK><<<grid, block, 0, st>>>(p, groups);
+  else
+    delta_chain_kernel<kOutBF16, DK><<<grid, block, 0, st>>>(p, groups);
+  return hipGetLastError();
 }
 
 template <int DK>
 hipError_t prefill_dk(const DPrefill &p, int out_type, hipStream_t st) {
   const int64_t chunks = (int64_t)p.rows / kChunk + p.n;
-  delta_chunk_kernel<DK><<<dim3((unsigned)(chunks * p.Hv)), dim3(64), 0, st>>>(p);
+  // Value heads of a chunk in one wave, which forms its k . k and k . q for all
+  // of them once: as many as leave 4 waves a SIMD.  8 value heads a key head,
+  // 2048 tokens: 170 us of 32 heads with 1 in a wave, 184 with 8; 428 us of 512
+  // heads with 1, 354 with 8 (both kernels).
+  const int per = (int)std::min<int64_t>(p.hpg, std::max<int64_t>(1, chunks * p.Hv / 4096));
+  const int waves = (p.hpg + per - 1) / per;
+  const int64_t ntiles = chunks * p.Hk * waves;
+  delta_chunk_kernel<DK><<<dim3(xcd_grid(ntiles)), dim3(64), 0, st>>>(p, per, waves, ntiles);
   const hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;
-  const int groups = (p.dv + kScanWaves * 16 - 1) / (kScanWaves * 16);
-  const dim3 grid((unsigned)((int64_t)p.n * p.Hv * groups)), block(kScanWaves * 64);
-  if (out_type == kOutF32)
-    delta_scan_kernel<kOutF32, DK><<<grid, block, 0, st>>>(p, groups);
-  else
-    delta_scan_kernel<kOutBF16, DK><<<grid, block, 0, st>>>(p, groups);
-  return hipGetLastError();
+  // Few chains: a workgroup to a block of 16 columns while each gets a CU of its
+  // own (2048 tokens, dim 128, us of chain, half-head, whole-head workgroups:
+  // 32 chains 89, 134, 181; 64 chains 162, 139, 185).  Many: a workgroup holds a
+  // whole head, two of them a CU (256 chains 554, 233, 213; 512 chains 917, 404,
+  // 338; 128 chains 302, 150, 193); up to 64 columns are four waves either way.
+  const int64_t chains = (int64_t)p.n * p.Hv;
+  if (chains * (p.dv / 16) <= 256) return chain_launch<DK>(p, out_type, st);
+  if (p.dv > 64 && chains >= 256) return scan_launch<DK, 8>(p, out_type, st);
+  return scan_launch<DK, 4>(p, out_type, st);
 }
 
 }  // namespace

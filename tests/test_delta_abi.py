@@ -163,6 +163,8 @@ def test_state_stride_refusals(stride, read, msg):
     (dict(initial_states=FAKE + 4), -1, "initial_states"),
     (dict(k=None), -1, "NULL"),
     (dict(k_row_stride=128), -1, "k_row_stride"),
+    (dict(q_row_stride=1 << 23), -2, "2^23"),
+    (dict(nheads_v=1 << 16, rows=0, num_seqs=1, v_row_stride=1 << 23), -2, "2^23"),
     (dict(workspace=None), -4, "workspace"),
     (dict(workspace_bytes=64), -4, "workspace"),
     (dict(workspace=FAKE + 4), -1, "workspace"),

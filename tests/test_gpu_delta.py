@@ -369,6 +369,37 @@ def test_prefill(lens, hk, hv, dk, dv, init, out_name):
     assert torch.equal(out3, out)
 
 
+# the chains (sequence, value head) that each scan kernel takes: up to 256 blocks of 16 columns one kernel, more another,
+# from 256 chains of more than 64 columns a third
+@pytest.mark.parametrize("n,most,hk,hv,dk,dv,init", [(9, 70, 2, 4, 128, 128, True), (20, 90, 4, 8, 64, 64, True),
+                                                     (20, 100, 2, 8, 128, 48, False), (40, 100, 4, 8, 128, 128, True),
+                                                     (33, 66, 2, 8, 64, 144, False), (64, 40, 1, 4, 64, 256, True)])
+def test_prefill_of_many_chains(n, most, hk, hv, dk, dv, init):
+    g = gen(n + dv)
+    lens = torch.randint(0, most + 1, (n,), generator=g).tolist()
+    lens[:3] = [most, 0, 33]
+    cu = [0]
+    for k in lens:
+        cu.append(cu[-1] + k)
+    x = R.inputs(g, cu[-1] + 3, hk, hv, dk, dv)
+    x["k"][cu[-1]:] = float("nan")
+    h0 = 0.3 * torch.randn(n, hv, dv, dk, generator=g) if init else None
+    h1 = torch.empty(n, hv, dv, dk, device=DEV)
+    out = torch.full((cu[-1] + 3, hv, dv), 7.0, dtype=torch.float32, device=DEV)
+    print("chains", n * hv, dk, dv, flush=True)
+    call_prefill(up(x), cu, out, None if h0 is None else h0.to(DEV), h1)
+    o, gt, h1 = out.cpu(), R.gates(x["dt"], x["beta"], x["A"], x["dt_bias"]), h1.cpu()
+    assert bool((o[cu[-1]:] == 7).all())
+    for s in list(range(4)) + [n // 2, n - 1]:
+        at = slice(cu[s], cu[s + 1])
+        S0 = h0[s] if init else torch.zeros(hv, dv, dk)
+        S, want = R.run(S0, x["q"][at], x["k"][at], x["v"][at], gt[0][at], gt[1][at], dk ** -0.5)
+        went = S0.double().flatten(1).norm(dim=1) + x["v"][at].double().transpose(0, 1).flatten(1).norm(dim=1)
+        windows = max(1, -(-lens[s] // 32))
+        R.check(o[at].transpose(0, 1), want.transpose(0, 1), went * dk ** -0.5, R.tol(dk, 32, windows, "f32"), "outputs %d" % s)
+        R.check(h1[s], S, went, R.tol(dk, 32, windows, "f32"), "state %d" % s)
+
+
 def test_prefill_without_rows():
     """Empty sequences only: the final states are the initial ones."""
     x = up(R.inputs(gen(11), 0, 1, 2, 64, 64))
