@@ -51,7 +51,7 @@ extern "C" {
  * (ssu_delta_init_state and ssu_delta_read_state convert from and to plain
  * row-major fp32).
  * Requirements: dim_k 64 or 128, dim_v a multiple of 16 in [16, 256],
- * nheads_v % nheads_k == 0, 1 <= ring_len <= 32, state_dtype SSU_F32, SSU_BF16
+ * nheads_v % nheads_k == 0, nheads_v * dim_v < 2^23, 1 <= ring_len <= 32, state_dtype SSU_F32, SSU_BF16
  * or SSU_F16, io_dtype SSU_BF16; pointers 16-byte aligned (gate_cache 8-byte,
  * ring_start and status 4-byte); strides at least one packed page and
  * multiples of 16 (gate_cache: of 8).  status may be NULL.
@@ -148,8 +148,8 @@ int ssu_delta_read_state(const ssu_delta_cache *cache, float *states, int64_t st
  * sequence whose cu_seqlens are negative, decreasing or past rows is skipped
  * and ORs SSU_STATUS_BAD_SEQLEN into *status (when not NULL).
  * Requirements: dim_k, dim_v and the heads as in ssu_delta_cache; rows *
- * nheads_v <= 2^30; num_seqs * nheads_v <= SSU_DELTA_MAX_PAIRS; nheads_v *
- * dim_v and the row strides below 2^23 elements.  num_seqs == 0
+ * nheads_v <= 2^30; num_seqs * nheads_v <= SSU_DELTA_MAX_PAIRS; row strides
+ * below 2^23 elements.  num_seqs == 0
  * is a no-op; with rows == 0 the per-row tensors may be NULL.
  */
 typedef struct ssu_delta_prefill_args {

@@ -23,6 +23,8 @@ int32_t raw(const E &e) {
   return v;
 }
 
+constexpr int64_t kWide = (int64_t)1 << 23;
+
 int check_dims(int32_t hk, int32_t hv, int32_t dk, int32_t dv) {
   if (hk < 1 || hv < 1) return api_fail(SSU_ERR_INVALID, "nheads_k and nheads_v must be positive (got %d, %d)", hk, hv);
   if (hv % hk != 0)
@@ -30,6 +32,8 @@ int check_dims(int32_t hk, int32_t hv, int32_t dk, int32_t dv) {
   if (dk != 64 && dk != 128) return api_fail(SSU_ERR_UNSUPPORTED, "dim_k must be 64 or 128 (got %d)", dk);
   if (dv < 16 || dv > ssu::kDeltaMaxDv || dv % 16 != 0)
     return api_fail(SSU_ERR_UNSUPPORTED, "dim_v must be a multiple of 16 in [16, %d] (got %d)", ssu::kDeltaMaxDv, dv);
+  if ((int64_t)hv * dv >= kWide)  // a few rows are addressed with 32-bit byte offsets
+    return api_fail(SSU_ERR_UNSUPPORTED, "nheads_v x dim_v must be below 2^23 (got %d x %d)", hv, dv);
   return SSU_OK;
 }
 
@@ -266,9 +270,8 @@ int ssu_delta_prefill(const ssu_delta_prefill_args *a, hipStream_t stream) {
     return api_fail(SSU_ERR_INVALID, "initial_states and final_states must be 16-byte aligned");
   rc = check_inputs(a, a->rows > 0, a->nheads_k, a->nheads_v, a->dim_k, a->dim_v);
   if (rc != SSU_OK) return rc;
-  const int64_t wide = (int64_t)1 << 23;  // a chunk's rows are addressed with 32-bit byte offsets
-  if ((int64_t)a->nheads_v * a->dim_v >= wide || a->q_row_stride >= wide || a->k_row_stride >= wide || a->v_row_stride >= wide)
-    return api_fail(SSU_ERR_UNSUPPORTED, "nheads_v x dim_v and the row strides must be below 2^23 elements");
+  if (a->q_row_stride >= kWide || a->k_row_stride >= kWide || a->v_row_stride >= kWide)  // as in check_dims
+    return api_fail(SSU_ERR_UNSUPPORTED, "the row strides must be below 2^23 elements");
   const size_t need = prefill_bytes(a->rows, a->num_seqs, a->nheads_v);
   if (!a->workspace || a->workspace_bytes < need)
     return api_fail(SSU_ERR_WORKSPACE, "the prefill needs a workspace of %zu bytes (got %zu%s)", need, a->workspace_bytes,

@@ -1,6 +1,13 @@
 // The gated delta rule on cached requests: step, flush, init and read
 // (one instantiation per checkpoint type).
 //
+// Both are bound by HBM, the checkpoint read once (and written once): 64
+// entries of 64 heads of 128 x 128, 4 new tokens, bf16, 33.8 us = 4.5 TB/s; 256
+// entries of up to 8, fp32, 260 us = 4.6 TB/s; folds of up to 8 tokens, bf16,
+// 58.3 us = 4.7 TB/s; 128 entries of up to 17, fp32, 220 us = 5.0 TB/s.  (A copy
+// reaches 4.75 TB/s.)  A wave's own time is latency: its vector instructions
+// are busy for a quarter of it, its matrix instructions for a tenth.
+//
 // Step.  With M = P T (P_ij = scale e^(G_i - G_j) q^_i . k^_j) the outputs need
 // neither U nor the state's products with k:
 //   o_i = S (scale e^(G_i) q^_i - sum_j M_ij b_j e^(G_j) k^_j) + sum_j M_ij b_j v_j,
@@ -63,135 +70,213 @@ __device__ __forceinline__ void state_encode(const float (&x)[DK / 4], u32x4 (&c
     }
 }
 
+// Loads and stores here are unconditional wherever they can be: after a branch
+// around one the compiler no longer knows what is in flight and waits for all
+// of it.  A word, row or row block that does not exist is read from the last
+// one that does (its weights are 0) and written past the end of a buffer
+// resource, where the hardware drops it.
+
 struct DEntry {
-  int slot, p, r, T, bos;
-  int mode;  // 0: nothing, 1: zero output rows, 2: replay
+  int slot, p, r, T, bos;  // slot, r: 0 unless mode is 2
+  int mode;                // 0: nothing, 1: zero output rows, 2: replay
 };
 
 __device__ __forceinline__ DEntry delta_entry(const DCache &c, const DStep &s, int b, bool report) {
+  const int32_t *cu = s.cu ? s.cu + b : s.slot_idx + b;  // (without cu_seqlens: any two words that exist)
+  int w0 = cu[0], w1 = cu[s.cu ? 1 : 0], slot = s.slot_idx[b], pn = s.pnat[b];
+  asm volatile("" : "+s"(w0), "+s"(w1), "+s"(slot), "+s"(pn));
   DEntry e;
-  e.bos = s.cu ? s.cu[b] : b * s.T;
-  e.T = s.cu ? s.cu[b + 1] - e.bos : s.T;
-  e.slot = s.slot_idx[b];
-  e.p = s.pnat[b];
-  e.r = 0;
+  e.bos = s.cu ? w0 : b * s.T;
+  e.T = s.cu ? w1 - w0 : s.T;
+  const bool there = slot > 0 && slot < c.num_slots;
+  const int ring = c.ring_start[there ? slot : 0];
+  e.p = pn;
+  e.r = ring;
   e.mode = 2;
   int bit = 0;
   if (e.T < 0 || e.T > s.T || e.bos < 0) {
     e.mode = 0;
     bit = SSU_STATUS_BAD_SEQLEN;
-  } else if (e.slot <= 0 || e.slot >= c.num_slots) {
+  } else if (!there) {
     e.mode = 1;
-  } else if (e.p < 0 || e.p > c.L - e.T) {
+  } else if (pn < 0 || pn > c.L - e.T) {
     e.mode = 1;
     bit = SSU_STATUS_BAD_PNAT;
-  } else {
-    e.r = c.ring_start[e.slot];
-    if (e.r < 0 || e.r >= c.L) {
-      e.mode = 1;
-      bit = SSU_STATUS_BAD_RING;
-    }
+  } else if (ring < 0 || ring >= c.L) {
+    e.mode = 1;
+    bit = SSU_STATUS_BAD_RING;
   }
+  e.slot = e.mode == 2 ? slot : 0;
   if (bit && report && c.status && threadIdx.x == 0) atomicOr(c.status, bit);
   return e;
 }
 
-constexpr int kStepWaveChunks = 16;  // 16-byte chunks of the checkpoint a lane keeps in flight
+// A wave's way over the row blocks of its share of a checkpoint: two sets of
+// registers of 8 KiB, a set loaded while the other one is worked on.  (64
+// entries of 64 bf16 heads, us of a step and a flush: 33.8 and 58.3; sets of 12
+// KiB 39.3 and 63.7, of 16 KiB 55 and 65.6; sets of 4 KiB with 3 waves a SIMD
+// instead of 2 32.8 and 57.8, but the fp32 forms spill then, 220 to 355 us.)
+constexpr int kSetChunks = 8;  // 16-byte chunks of a lane per set
+template <int ST, int DK>
+struct Rows {
+  static constexpr int CH = dchunks(ST, DK), RB = kSetChunks / CH;  // row blocks of a set
+  u32x4 st[2][RB][CH];
+  const uint8_t *base;  // the share's first row block, this lane's chunk 0
+  int nrb;
+
+  __device__ __forceinline__ void load(int set, int first) {
+#pragma unroll
+    for (int i = 0; i < RB; ++i) {
+      const uint8_t *at = base + (uint32_t)(min(first + i, nrb - 1) * (CH * 1024));
+#pragma unroll
+      for (int u = 0; u < CH; ++u) st[set][i][u] = ld16_nt(at + u * 1024);
+    }
+  }
+};
+
+// The k and v rows of a window on their way to LDS (kw [KW][DK + 8], vw
+// [KW][VS]) through registers.  row(t, new) gives a token's row in a ring
+// (t < p) or among the new rows.
+template <int KW, int DK>
+struct Window {
+  static constexpr int PK = KW * DK / 8 / 64, PV = KW * 16 / 64, KS = DK + 8;
+  u32x4 k[PK], v[PV];
+  int p, W, r, L;
+  const uint8_t *ring_k, *ring_v, *new_k, *new_v;  // new_*: row of the first new token
+  int64_t k_step, v_step;                          // bytes between new rows
+  int dv;
+
+  __device__ __forceinline__ const uint8_t *row(int t, const uint8_t *ring, int ring_row, const uint8_t *fresh, int64_t step) const {
+    t = min(t, W - 1);
+    return t < p ? ring + (uint32_t)(ring_pos(r, t, L) * ring_row) : fresh + (int64_t)(t - p) * step;
+  }
+  __device__ __forceinline__ void fetch_k(int lane) {
+#pragma unroll
+    for (int i = 0; i < PK; ++i) {
+      const int at = i * 64 + lane;
+      k[i] = ld16(row(at / (DK / 8), ring_k, DK * 2, new_k, k_step) + at % (DK / 8) * 16);
+    }
+  }
+  __device__ __forceinline__ void fetch_v(int lane, int c0) {  // columns c0 .. c0 + 127
+#pragma unroll
+    for (int i = 0; i < PV; ++i) {
+      const int at = i * 64 + lane;
+      v[i] = ld16(row(at / 16, ring_v, dv * 2, new_v, v_step) + min(c0 + at % 16 * 8, dv - 8) * 2);
+    }
+  }
+  __device__ __forceinline__ void store_k(uint16_t *kw, int lane) const {
+#pragma unroll
+    for (int i = 0; i < PK; ++i) {
+      const int at = i * 64 + lane;
+      st16(kw + at / (DK / 8) * KS + at % (DK / 8) * 8, k[i]);
+    }
+  }
+  // all but the last 128 columns of v (which are left on their way), for dim_v over 128
+  __device__ __forceinline__ int pass_v(uint16_t *vw, int VS, int lane) {
+    int c0 = 0;
+    fetch_v(lane, 0);
+    for (; c0 + 128 < dv; c0 += 128) {
+      store_v(vw, VS, lane, c0);
+      fetch_v(lane, c0 + 128);
+    }
+    return c0;
+  }
+  __device__ __forceinline__ void store_v(uint16_t *vw, int VS, int lane, int c0) const {
+#pragma unroll
+    for (int i = 0; i < PV; ++i) {
+      const int at = i * 64 + lane;
+      st16(vw + at / 16 * VS + c0 + at % 16 * 8, v[i]);
+    }
+  }
+};
+
+// Row stride of the window's v in LDS: dim_v in whole pieces of 128 columns.
+__device__ __host__ __forceinline__ int v_stride(int dv) { return (dv + 127) / 128 * 128 + 8; }
+
+// A token's row from LDS in the order of the checkpoint's operands: depth step
+// u holds n = 32 u + 16 a + 4 q + r.
+__device__ __forceinline__ bf16x8 operand_row(const uint16_t *row, int u, int q) {
+  struct { u32x2 a, b; } f = {ld8(row + 32 * u + 4 * q), ld8(row + 32 * u + 16 + 4 * q)};
+  return __builtin_bit_cast(bf16x8, f);
+}
 
 template <int ST, int OT, int KW, int DK>
-__global__ __launch_bounds__(64, 2) void delta_step_kernel(DCache c, DStep s, int parts, int64_t nwaves) {
-  constexpr int CH = dchunks(ST, DK), RB = kStepWaveChunks / CH, E = KW / 4;
-  constexpr int NQ = OT == kOutF32 ? 3 : 2, NS = ST == kF32 ? NQ : (ST == kF16 ? 2 : 1);
-  constexpr int VS = RB * 16 + 8;
+__global__ __launch_bounds__(64, 2) void delta_step_kernel(DCache c, DStep s, int parts, int share, int nwaves) {
+  constexpr int E = KW / 4, NQ = OT == kOutF32 ? 3 : 2, NS = ST == kF32 ? NQ : (ST == kF16 ? 2 : 1);
   typedef typename Tok<KW>::V TV;
-  constexpr int KS = DK + 8;  // row strides in LDS: 8 values on, so 16 rows start in different banks
+  typedef Rows<ST, DK> Tiles;
+  typedef Window<KW, DK> Win;
   __shared__ WinLds<KW> w;
   __shared__ float rq[16];
-  __shared__ __align__(16) uint16_t kw[KW * KS], vw[KW * VS];
+  __shared__ __align__(16) uint16_t kw[KW * Win::KS];
+  extern __shared__ __align__(16) uint16_t vw[];
+  const int VS = v_stride(c.dv);
 
-  const int64_t tile = xcd_tile(blockIdx.x, gridDim.x);
+  const int tile = (int)xcd_tile(blockIdx.x, gridDim.x);
   if (tile >= nwaves) return;
   const int lane = threadIdx.x, m = lane & 15, q = lane >> 4;
-  const int part = (int)(tile % parts);
-  const int64_t pair = tile / parts;
-  const int h = (int)(pair % c.Hv), b = (int)(pair / c.Hv), hk = h / c.hpg;
+  const int part = tile % parts, pair = tile / parts, h = pair % c.Hv, b = pair / c.Hv, hk = h / c.hpg;
   const DEntry e = delta_entry(c, s, b, part == 0 && h == 0);
   if (e.mode == 0 || e.T == 0) return;
-  const int rb0 = part * RB, nrb = min(RB, c.dv / 16 - rb0);
+  const int rb0 = part * share;
+  constexpr int kOut = OT == kOutF32 ? 4 : 2;
+  const int row_bytes = c.Hv * c.dv * kOut;
+  const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(static_cast<uint8_t *>(s.out) + (int64_t)e.bos * row_bytes, 0,
+                                                      e.T * row_bytes, 0x00020000);
+  Tiles rows;
+  rows.nrb = min(share, c.dv / 16 - rb0);
+  // this lane's outputs: token m, four columns of a row block
+  const int out_at = m < e.T ? m * row_bytes + (h * c.dv + rb0 * 16 + 4 * q) * kOut : 0x7FFF0000;
   if (e.mode == 1) {
-    for (int i = lane; i < e.T * nrb * 4; i += 64) {
-      const int t = i / (nrb * 4), ch = i % (nrb * 4);
-      const int64_t o = ((int64_t)(e.bos + t) * c.Hv + h) * c.dv + rb0 * 16 + ch * 4;
+    for (int i = 0; i < rows.nrb; ++i) {
       if constexpr (OT == kOutF32)
-        st16(static_cast<float *>(s.out) + o, u32x4{0, 0, 0, 0});
+        __builtin_amdgcn_raw_buffer_store_b128(u32x4{0, 0, 0, 0}, rsrc, out_at + i * 64, 0, 0);
       else
-        st8(static_cast<uint16_t *>(s.out) + o, u32x2{0, 0});
+        __builtin_amdgcn_raw_buffer_store_b64(u32x2{0, 0}, rsrc, out_at + i * 32, 0, 0);
     }
     return;
   }
 
-  // the checkpoint rows, on their way while the queries are formed
-  u32x4 st[RB][CH];
-  {
-    const uint8_t *src = c.state + (int64_t)e.slot * c.state_stride +
-                         ((int64_t)h * c.dv / 16 + rb0) * (CH * 1024) + lane * 16;
-#pragma unroll
-    for (int i = 0; i < RB; ++i)
-#pragma unroll
-      for (int u = 0; u < CH; ++u)
-        st[i][u] = i < nrb ? ld16_nt(src + (i * CH + u) * 1024) : u32x4{0, 0, 0, 0};
-  }
-
-  // the window: p live tokens of the ring, then the new ones; behind it zeros
-  const int p = e.p, W = p + e.T;
+  // everything on its way: the window (p live tokens of the ring, then the new
+  // ones), its gates, the queries, then the checkpoint's first rows
+  const int p = e.p;
   uint8_t *ring_k = c.kc + (int64_t)e.slot * c.k_stride + (int64_t)hk * c.L * DK * 2;
   uint8_t *ring_v = c.vc + (int64_t)e.slot * c.v_stride + (int64_t)h * c.L * c.dv * 2;
   float2 *ring_g = reinterpret_cast<float2 *>(c.gc + (int64_t)e.slot * c.g_stride) + (int64_t)h * c.L;
-  const bool first = part == 0, first_k = first && h % c.hpg == 0;
-#pragma unroll
-  for (int i = 0; i < KW * (DK / 8) / 64; ++i) {
-    const int t = (i * 64 + lane) / (DK / 8), ch = (i * 64 + lane) % (DK / 8);
-    u32x4 v = {0, 0, 0, 0};
-    if (t < W) {
-      uint8_t *at = ring_k + (ring_pos(e.r, t, c.L) * DK + ch * 8) * 2;
-      v = t < p ? ld16(at) : ld16(s.k + (int64_t)(e.bos + t - p) * s.k_stride + hk * DK + ch * 8);
-      if (t >= p && first_k) st16(at, v);
-    }
-    st16(kw + t * KS + ch * 8, v);
-  }
-#pragma unroll
-  for (int i = 0; i < (KW * RB * 2 + 63) / 64; ++i) {
-    const int at = i * 64 + lane, t = at / (RB * 2), ch = at % (RB * 2);
-    if (at < KW * RB * 2) {
-      u32x4 v = {0, 0, 0, 0};
-      if (t < W && ch < nrb * 2) {
-        uint8_t *dst = ring_v + ((int64_t)ring_pos(e.r, t, c.L) * c.dv + rb0 * 16 + ch * 8) * 2;
-        v = t < p ? ld16(dst) : ld16(s.v + (int64_t)(e.bos + t - p) * s.v_stride + h * c.dv + rb0 * 16 + ch * 8);
-        if (t >= p) st16(dst, v);
-      }
-      st16(vw + t * VS + ch * 8, v);
-    }
-  }
-  bf16x8 qn[DK / 32];
+  Win win;
+  win.p = p;
+  win.W = p + e.T;
+  win.r = e.r;
+  win.L = c.L;
+  win.dv = c.dv;
+  win.ring_k = ring_k;
+  win.ring_v = ring_v;
+  win.new_k = reinterpret_cast<const uint8_t *>(s.k + (int64_t)e.bos * s.k_stride + hk * DK);
+  win.new_v = reinterpret_cast<const uint8_t *>(s.v + (int64_t)e.bos * s.v_stride + h * c.dv);
+  win.k_step = s.k_stride * 2;
+  win.v_step = s.v_stride * 2;
+  win.fetch_k(lane);
+  const int64_t gate_row = (int64_t)(e.bos + min(max(lane - p, 0), e.T - 1)) * c.Hv + h;
+  const float dt = s.dt[gate_row], beta = s.beta[gate_row], A = s.A[h], bias = s.dt_bias[h];
+  const float2 old = ring_g[ring_pos(e.r, min(lane, win.W - 1), c.L)];
   u32x2 qd[DK / 16];
   {
-    const uint16_t *qr = s.q + (int64_t)(e.bos + (m < e.T ? m : 0)) * s.q_stride + hk * DK;
+    const uint16_t *qr = s.q + (int64_t)(e.bos + min(m, e.T - 1)) * s.q_stride + hk * DK + 4 * q;
 #pragma unroll
-    for (int u = 0; u < DK / 32; ++u) qn[u] = __builtin_bit_cast(bf16x8, ld16(qr + (4 * u + q) * 8));
-#pragma unroll
-    for (int t = 0; t < DK / 16; ++t) qd[t] = ld8(qr + 16 * t + 4 * q);
+    for (int t = 0; t < DK / 16; ++t) qd[t] = ld8(qr + 16 * t);
   }
-  float2 gb = {0.f, 0.f};
-  if (lane < W) {
-    float2 *at = ring_g + ring_pos(e.r, lane, c.L);
-    if (lane < p) {
-      gb = *at;
-    } else {
-      const int64_t o = (int64_t)(e.bos + lane - p) * c.Hv + h;
-      gb = delta_gate(s.dt[o], s.beta[o], s.A[h], s.dt_bias[h], s.softplus, s.sigmoid);
-      if (first) *at = gb;
-    }
-  }
+  const int v0 = win.pass_v(vw, VS, lane);
+  rows.base = c.state + (int64_t)e.slot * c.state_stride + ((int64_t)h * c.dv / 16 + rb0) * (Tiles::CH * 1024) + lane * 16;
+  rows.load(0, 0);
+  rows.load(1, Tiles::RB);
+
+  win.store_k(kw, lane);
+  win.store_v(vw, VS, lane, v0);
+  float2 gb = delta_gate(dt, beta, A, bias, s.softplus, s.sigmoid);
+  const bool fresh = lane >= p && lane < win.W;
+  if (lane < p) gb = old;
+  const float2 append = gb;
+  if (lane >= win.W) gb = float2{0.f, 0.f};
   const double G = scan_d<KW>((double)gb.x * kLog2e, lane);
   if (lane < KW) {
     w.G[lane] = G;
@@ -207,13 +292,15 @@ __global__ __launch_bounds__(64, 2) void delta_step_kernel(DCache c, DStep s, in
   for (int t = 0; t < KW / 16; ++t) qk[t] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int u = 0; u < DK / 32; ++u) {
+    struct { u32x2 a, b; } qp = {qd[2 * u], qd[2 * u + 1]};
+    const bf16x8 qf = __builtin_bit_cast(bf16x8, qp);
     bf16x8 f[KW / 16];
 #pragma unroll
     for (int t = 0; t < KW / 16; ++t) {
-      f[t] = __builtin_bit_cast(bf16x8, ld16(kw + (16 * t + m) * KS + (4 * u + q) * 8));
-      qk[t] = mfma_bf16(f[t], qn[u], qk[t]);
+      f[t] = operand_row(kw + (16 * t + m) * Win::KS, u, q);
+      qk[t] = mfma_bf16(f[t], qf, qk[t]);
     }
-    qq = mfma_bf16(qn[u], qn[u], qq);
+    qq = mfma_bf16(qf, qf, qq);
     gram_kk<KW>(f, kk);
   }
   write_rk<KW>(w, m, q, kk, c.norm);
@@ -255,42 +342,61 @@ __global__ __launch_bounds__(64, 2) void delta_step_kernel(DCache c, DStep s, in
   bf16x8 fq[DK / 32][NQ];
   {
     const float eq = rqm * exp2_d(Gm);
-    float y[DK / 4];
-#pragma unroll
-    for (int t = 0; t < DK / 16; ++t) {
-      f32x4 acc = {eq * bf2f(qd[t][0] & 0xFFFFu), eq * __uint_as_float(qd[t][0] & 0xFFFF0000u),
-                   eq * bf2f(qd[t][1] & 0xFFFFu), eq * __uint_as_float(qd[t][1] & 0xFFFF0000u)};
-      acc = Tok<KW>::template exact<true>(Tok<KW>::load_tr(kw, KS, 16 * t, lane), fk, acc);
-#pragma unroll
-      for (int r = 0; r < 4; ++r) y[4 * t + r] = acc[r];
-    }
 #pragma unroll
     for (int ks = 0; ks < DK / 32; ++ks) {
       float z[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) z[i] = y[8 * ks + i];
+      for (int a = 0; a < 2; ++a) {
+        const int t = 2 * ks + a;
+        f32x4 acc = {eq * bf2f(qd[t][0] & 0xFFFFu), eq * __uint_as_float(qd[t][0] & 0xFFFF0000u),
+                     eq * bf2f(qd[t][1] & 0xFFFFu), eq * __uint_as_float(qd[t][1] & 0xFFFF0000u)};
+        acc = Tok<KW>::template exact<true>(Tok<KW>::load_tr(kw, Win::KS, 16 * t, lane), fk, acc);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) z[4 * a + r] = acc[r];
+      }
       split<NQ>(z, fq[ks]);
     }
   }
 
+  // the readout, a set of row blocks after the other
+  auto readout = [&](int set, int first) {
 #pragma unroll
-  for (int i = 0; i < RB; ++i) {
-    if (i >= nrb) break;
-    f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+    for (int i = 0; i < Tiles::RB; ++i) {
+      f32x4 acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int ks = 0; ks < DK / 32; ++ks) {
-      bf16x8 f[NS];
-      state_operand<ST, DK, NS>(st[i], ks, f);
-      acc = mfma_parts(f, fq[ks], acc);
-    }
-    acc = Tok<KW>::template exact<true>(Tok<KW>::load_tr(vw, VS, 16 * i, lane), fv, acc);
-    if (m < e.T) {
-      const int64_t o = ((int64_t)(e.bos + m) * c.Hv + h) * c.dv + (rb0 + i) * 16 + 4 * q;
+      for (int ks = 0; ks < DK / 32; ++ks) {
+        bf16x8 f[NS];
+        state_operand<ST, DK, NS>(rows.st[set][i], ks, f);
+        acc = mfma_parts(f, fq[ks], acc);
+      }
+      const int rb = min(first + i, rows.nrb - 1);
+      acc = Tok<KW>::template exact<true>(Tok<KW>::load_tr(vw, VS, (rb0 + rb) * 16, lane), fv, acc);
+      const int to = first + i < rows.nrb ? out_at : 0x7FFF0000;
       if constexpr (OT == kOutF32)
-        st16(static_cast<float *>(s.out) + o, __builtin_bit_cast(u32x4, acc));
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, acc), rsrc, to + rb * 64, 0, 0);
       else
-        st8(static_cast<uint16_t *>(s.out) + o, u32x2{pack_bf16(acc[0], acc[1]), pack_bf16(acc[2], acc[3])});
+        __builtin_amdgcn_raw_buffer_store_b64(u32x2{pack_bf16(acc[0], acc[1]), pack_bf16(acc[2], acc[3])}, rsrc, to + rb * 32, 0, 0);
     }
+  };
+  for (int first = 0; first < rows.nrb; first += 2 * Tiles::RB) {
+    readout(0, first);
+    rows.load(0, first + 2 * Tiles::RB);
+    readout(1, first + Tiles::RB);
+    rows.load(1, first + 3 * Tiles::RB);
+  }
+
+  // the new tokens appended: k by a group's first head, v by each share, the
+  // gates by a head's first share
+  if (part == 0 && fresh) ring_g[ring_pos(e.r, lane, c.L)] = append;
+  if (part == 0 && h % c.hpg == 0) {
+    for (int i = lane; i < e.T * (DK / 8); i += 64) {
+      const int t = p + i / (DK / 8), ch = i % (DK / 8);
+      st16(ring_k + (uint32_t)(ring_pos(e.r, t, c.L) * DK + ch * 8) * 2, ld16(kw + t * Win::KS + ch * 8));
+    }
+  }
+  for (int i = lane; i < e.T * rows.nrb * 2; i += 64) {
+    const int t = p + i / (rows.nrb * 2), col = rb0 * 16 + i % (rows.nrb * 2) * 8;
+    st16(ring_v + (uint32_t)(ring_pos(e.r, t, c.L) * c.dv + col) * 2, ld16(vw + t * VS + col));
   }
 }
 
@@ -310,51 +416,48 @@ __device__ __forceinline__ bool delta_fold_entry(const DCache &c, int slot, int 
 
 template <int ST, int KW, int DK>
 __global__ __launch_bounds__(64, 2) void delta_flush_kernel(DCache c, const int32_t *slot_idx, const int32_t *num_fold,
-                                                         int parts, int64_t nwaves) {
-  constexpr int CH = dchunks(ST, DK), RB = kStepWaveChunks / CH, E = KW / 4, NT = KW / 16;
-  constexpr int NW = ST == kF32 ? 3 : 2, NS = ST == kBF16 ? 1 : 2;
-  constexpr int VS = RB * 16 + 8;
+                                                            int parts, int share, int nwaves) {
+  constexpr int E = KW / 4, NT = KW / 16, NW = ST == kF32 ? 3 : 2, NS = ST == kBF16 ? 1 : 2;
   typedef typename Tok<KW>::V TV;
-  constexpr int KS = DK + 8;
+  typedef Rows<ST, DK> Tiles;
+  typedef Window<KW, DK> Win;
   __shared__ WinLds<KW> w;
-  __shared__ __align__(16) uint16_t kw[KW * KS], vw[KW * VS];
+  __shared__ __align__(16) uint16_t kw[KW * Win::KS];
+  extern __shared__ __align__(16) uint16_t vw[];
+  const int VS = v_stride(c.dv);
 
-  const int64_t tile = xcd_tile(blockIdx.x, gridDim.x);
+  const int tile = (int)xcd_tile(blockIdx.x, gridDim.x);
   if (tile >= nwaves) return;
   const int lane = threadIdx.x, m = lane & 15, q = lane >> 4;
-  const int part = (int)(tile % parts);
-  const int64_t pair = tile / parts;
-  const int h = (int)(pair % c.Hv), b = (int)(pair / c.Hv), hk = h / c.hpg;
+  const int part = tile % parts, pair = tile / parts, h = pair % c.Hv, b = pair / c.Hv, hk = h / c.hpg;
   const int slot = slot_idx[b], k = num_fold[b];
   int ring = 0;
   if (!delta_fold_entry(c, slot, k, ring, part == 0 && h == 0 && lane == 0)) return;
-  const int rb0 = part * RB, nrb = min(RB, c.dv / 16 - rb0);
-
-  uint8_t *tiles = c.state + (int64_t)slot * c.state_stride + ((int64_t)h * c.dv / 16 + rb0) * (CH * 1024) + lane * 16;
-  u32x4 st[RB][CH];
-#pragma unroll
-  for (int i = 0; i < RB; ++i)
-#pragma unroll
-    for (int u = 0; u < CH; ++u) st[i][u] = i < nrb ? ld16_nt(tiles + (i * CH + u) * 1024) : u32x4{0, 0, 0, 0};
-
-  const uint8_t *ring_k = c.kc + (int64_t)slot * c.k_stride + (int64_t)hk * c.L * DK * 2;
-  const uint8_t *ring_v = c.vc + (int64_t)slot * c.v_stride + (int64_t)h * c.L * c.dv * 2;
+  const int rb0 = part * share;
+  Win win;
+  win.p = win.W = k;  // ring tokens only
+  win.r = ring;
+  win.L = c.L;
+  win.dv = c.dv;
+  win.ring_k = c.kc + (int64_t)slot * c.k_stride + (int64_t)hk * c.L * DK * 2;
+  win.ring_v = c.vc + (int64_t)slot * c.v_stride + (int64_t)h * c.L * c.dv * 2;
+  win.new_k = win.new_v = nullptr;
+  win.k_step = win.v_step = 0;
+  win.fetch_k(lane);
   const float2 *ring_g = reinterpret_cast<const float2 *>(c.gc + (int64_t)slot * c.g_stride) + (int64_t)h * c.L;
-#pragma unroll
-  for (int i = 0; i < KW * (DK / 8) / 64; ++i) {
-    const int t = (i * 64 + lane) / (DK / 8), ch = (i * 64 + lane) % (DK / 8);
-    st16(kw + t * KS + ch * 8,
-         t < k ? ld16(ring_k + (ring_pos(ring, t, c.L) * DK + ch * 8) * 2) : u32x4{0, 0, 0, 0});
-  }
-#pragma unroll
-  for (int i = 0; i < (KW * RB * 2 + 63) / 64; ++i) {
-    const int at = i * 64 + lane, t = at / (RB * 2), ch = at % (RB * 2);
-    if (at < KW * RB * 2)
-      st16(vw + t * VS + ch * 8, t < k && ch < nrb * 2
-                                     ? ld16(ring_v + ((int64_t)ring_pos(ring, t, c.L) * c.dv + rb0 * 16 + ch * 8) * 2)
-                                     : u32x4{0, 0, 0, 0});
-  }
-  const float2 gb = lane < k ? ring_g[ring_pos(ring, lane, c.L)] : float2{0.f, 0.f};
+  float2 gb = ring_g[ring_pos(ring, min(lane, k - 1), c.L)];
+  const int v0 = win.pass_v(vw, VS, lane);
+  Tiles rows;
+  rows.nrb = min(share, c.dv / 16 - rb0);
+  uint8_t *tiles = c.state + (int64_t)slot * c.state_stride + ((int64_t)h * c.dv / 16 + rb0) * (Tiles::CH * 1024);
+  rows.base = tiles + lane * 16;
+  rows.load(0, 0);
+  rows.load(1, Tiles::RB);
+  const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(tiles, 0, rows.nrb * Tiles::CH * 1024, 0x00020000);
+
+  win.store_k(kw, lane);
+  win.store_v(vw, VS, lane, v0);
+  if (lane >= k) gb = float2{0.f, 0.f};
   const double G = scan_d<KW>((double)gb.x * kLog2e, lane);
   if (lane < KW) {
     w.G[lane] = G;
@@ -369,7 +472,7 @@ __global__ __launch_bounds__(64, 2) void delta_flush_kernel(DCache c, const int3
     for (int u = 0; u < DK / 32; ++u) {
       bf16x8 f[NT];
 #pragma unroll
-      for (int t = 0; t < NT; ++t) f[t] = __builtin_bit_cast(bf16x8, ld16(kw + (16 * t + m) * KS + (4 * u + q) * 8));
+      for (int t = 0; t < NT; ++t) f[t] = operand_row(kw + (16 * t + m) * Win::KS, u, q);
       gram_kk<KW>(f, kk);
     }
     write_rk<KW>(w, m, q, kk, c.norm);
@@ -379,11 +482,11 @@ __global__ __launch_bounds__(64, 2) void delta_flush_kernel(DCache c, const int3
   wave_sync();
   invert_diag<KW>(w, lane);
 
-  // T b (towards V) and W = T b e^G K^ as operands, rows = tokens
-  TV ft[NT][NW], kt[DK / 16];
+  // T b (towards V) and W = T b e^G K^ as operands, rows = tokens.  W and an
+  // fp32 checkpoint's values enter their product in two parts (the residuals
+  // it goes into are what the fold adds, not the checkpoint itself).
+  TV ft[NT][NW];
   bf16x8 fw[NT][DK / 32][2];
-#pragma unroll
-  for (int t = 0; t < DK / 16; ++t) kt[t] = Tok<KW>::load_tr(kw, KS, 16 * t, lane);
   float bj[E], ej[E];
 #pragma unroll
   for (int a = 0; a < NT; ++a)
@@ -410,7 +513,7 @@ __global__ __launch_bounds__(64, 2) void delta_flush_kernel(DCache c, const int3
       float z[8];
 #pragma unroll
       for (int a = 0; a < 2; ++a) {
-        const f32x4 acc = Tok<KW>::template exact<true>(kt[2 * ks + a], fy, f32x4{0.f, 0.f, 0.f, 0.f});
+        const f32x4 acc = Tok<KW>::template exact<true>(Tok<KW>::load_tr(kw, Win::KS, 32 * ks + 16 * a, lane), fy, f32x4{0.f, 0.f, 0.f, 0.f});
 #pragma unroll
         for (int r = 0; r < 4; ++r) z[4 * a + r] = acc[r];
       }
@@ -428,38 +531,50 @@ __global__ __launch_bounds__(64, 2) void delta_flush_kernel(DCache c, const int3
       fu[4 * a + r] = exp2_d(Gw - w.G[j]) * w.rk[j];
     }
 
+  auto fold = [&](int set, int first) {
 #pragma unroll
-  for (int i = 0; i < RB; ++i) {
-    if (i >= nrb) break;
-    bf16x8 f[DK / 32][NS];
+    for (int i = 0; i < Tiles::RB; ++i) {
+      __builtin_amdgcn_sched_barrier(0);  // one row block's values at a time: two would spill
+      const u32x4(&st)[Tiles::CH] = rows.st[set][i];
+      const int rb = min(first + i, rows.nrb - 1);
+      const TV vt = Tok<KW>::load_tr(vw, VS, (rb0 + rb) * 16, lane);
+      f32x4 acc[NT];
 #pragma unroll
-    for (int ks = 0; ks < DK / 32; ++ks) state_operand<ST, DK, NS>(st[i], ks, f[ks]);
-    const TV vt = Tok<KW>::load_tr(vw, VS, 16 * i, lane);
-    float u[E];
+      for (int ti = 0; ti < NT; ++ti) acc[ti] = Tok<KW>::template exact<false>(vt, ft[ti], f32x4{0.f, 0.f, 0.f, 0.f});
 #pragma unroll
-    for (int ti = 0; ti < NT; ++ti) {
-      f32x4 acc = Tok<KW>::template exact<false>(vt, ft[ti], f32x4{0.f, 0.f, 0.f, 0.f});
+      for (int ks = 0; ks < DK / 32; ++ks) {
+        bf16x8 f[NS];
+        state_operand<ST, DK, NS>(st, ks, f);
 #pragma unroll
-      for (int ks = 0; ks < DK / 32; ++ks) acc = mfma_parts(fw[ti][ks], f[ks], acc);
+        for (int ti = 0; ti < NT; ++ti) acc[ti] = mfma_parts(fw[ti][ks], f, acc[ti]);
+      }
+      float u[E];
 #pragma unroll
-      for (int r = 0; r < 4; ++r) u[4 * ti + r] = acc[r] * fu[4 * ti + r];
+      for (int a = 0; a < E; ++a) u[a] = acc[a / 4][a % 4] * fu[a];
+      TV fuu[NW];
+      split<NW>(u, fuu);
+      float y[DK / 4];
+#pragma unroll
+      for (int t = 0; t < DK / 16; ++t) {
+        f32x4 z;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) z[r] = ew * state_value<ST>(st, 4 * t + r);
+        z = Tok<KW>::template exact<true>(Tok<KW>::load_tr(kw, Win::KS, 16 * t, lane), fuu, z);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) y[4 * t + r] = z[r];
+      }
+      u32x4 o[Tiles::CH];
+      state_encode<ST, DK>(y, o);
+      const int to = first + i < rows.nrb ? rb * (Tiles::CH * 1024) + lane * 16 : 0x7FFF0000;
+#pragma unroll
+      for (int v = 0; v < Tiles::CH; ++v) __builtin_amdgcn_raw_buffer_store_b128(o[v], rsrc, to, v * 1024, 2);
     }
-    TV fuu[NW];
-    split<NW>(u, fuu);
-    float y[DK / 4];
-#pragma unroll
-    for (int t = 0; t < DK / 16; ++t) {
-      f32x4 acc;
-#pragma unroll
-      for (int r = 0; r < 4; ++r) acc[r] = ew * state_value<ST>(st[i], 4 * t + r);
-      acc = Tok<KW>::template exact<true>(kt[t], fuu, acc);
-#pragma unroll
-      for (int r = 0; r < 4; ++r) y[4 * t + r] = acc[r];
-    }
-    u32x4 o[CH];
-    state_encode<ST, DK>(y, o);
-#pragma unroll
-    for (int v = 0; v < CH; ++v) st16_nt(tiles + (i * CH + v) * 1024, o[v]);
+  };
+  for (int first = 0; first < rows.nrb; first += 2 * Tiles::RB) {
+    fold(0, first);
+    rows.load(0, first + 2 * Tiles::RB);
+    fold(1, first + Tiles::RB);
+    rows.load(1, first + 3 * Tiles::RB);
   }
 }
 
@@ -527,41 +642,45 @@ __global__ __launch_bounds__(64) void delta_state_kernel(DCache c, float *states
 // launches
 // ---------------------------------------------------------------------------
 
+// Row blocks of a head in one wave's share: all of them, since every share forms
+// the window's part again, unless that leaves fewer waves than 1024 (fp32) or
+// 512 (16-bit checkpoints).  Steps of heads of 128 x 128 with 1024, 2048 and
+// 4096 waves wanted: 512 pairs fp32 11.4, 13.3, 20.3 us, 1024 pairs bf16 11.3,
+// 14.0, 19.7 us; with 64 wanted: 64 pairs fp32 8.4 us against 7.0.
 template <int ST, int DK>
-hipError_t delta_step_dk(const DCache &c, const DStep &s, int out_type, hipStream_t st) {
-  constexpr int RB = kStepWaveChunks / dchunks(ST, DK);
-  const int parts = (c.dv / 16 + RB - 1) / RB;
-  const int64_t nwaves = (int64_t)s.batch * c.Hv * parts;
+int wave_share(int64_t pairs, int nrb) {
+  constexpr int kSet = Rows<ST, DK>::RB, kWant = ST == kF32 ? 1024 : 512;
+  int share = nrb;
+  while (share > kSet && pairs * ((nrb + share - 1) / share) < kWant) share = (share + 1) / 2;
+  return (share + kSet - 1) / kSet * kSet;
+}
+
+template <int KW>
+size_t window_lds(int dv) { return (size_t)KW * v_stride(dv) * 2; }
+
+template <int ST, int KW, int DK>
+hipError_t delta_step_kw(const DCache &c, const DStep &s, int out_type, hipStream_t st) {
+  const int share = wave_share<ST, DK>((int64_t)s.batch * c.Hv, c.dv / 16), parts = (c.dv / 16 + share - 1) / share;
+  const int nwaves = s.batch * c.Hv * parts;
   const dim3 grid(xcd_grid(nwaves)), block(64);
-  if (out_type == kOutF32) {
-    if (c.L <= 16)
-      delta_step_kernel<ST, kOutF32, 16, DK><<<grid, block, 0, st>>>(c, s, parts, nwaves);
-    else
-      delta_step_kernel<ST, kOutF32, 32, DK><<<grid, block, 0, st>>>(c, s, parts, nwaves);
-  } else {
-    if (c.L <= 16)
-      delta_step_kernel<ST, kOutBF16, 16, DK><<<grid, block, 0, st>>>(c, s, parts, nwaves);
-    else
-      delta_step_kernel<ST, kOutBF16, 32, DK><<<grid, block, 0, st>>>(c, s, parts, nwaves);
-  }
+  if (out_type == kOutF32)
+    delta_step_kernel<ST, kOutF32, KW, DK><<<grid, block, window_lds<KW>(c.dv), st>>>(c, s, parts, share, nwaves);
+  else
+    delta_step_kernel<ST, kOutBF16, KW, DK><<<grid, block, window_lds<KW>(c.dv), st>>>(c, s, parts, share, nwaves);
   return hipGetLastError();
 }
 
 template <int ST>
 hipError_t delta_step_st(const DCache &c, const DStep &s, int out_type, hipStream_t st) {
-  return c.dk == 64 ? delta_step_dk<ST, 64>(c, s, out_type, st) : delta_step_dk<ST, 128>(c, s, out_type, st);
+  if (c.dk == 64) return c.L <= 16 ? delta_step_kw<ST, 16, 64>(c, s, out_type, st) : delta_step_kw<ST, 32, 64>(c, s, out_type, st);
+  return c.L <= 16 ? delta_step_kw<ST, 16, 128>(c, s, out_type, st) : delta_step_kw<ST, 32, 128>(c, s, out_type, st);
 }
 
-template <int ST, int DK>
-hipError_t delta_flush_dk(const DCache &c, const int32_t *slot_idx, const int32_t *num_fold, int n, hipStream_t st) {
-  constexpr int RB = kStepWaveChunks / dchunks(ST, DK);
-  const int parts = (c.dv / 16 + RB - 1) / RB;
-  const int64_t nwaves = (int64_t)n * c.Hv * parts;
-  const dim3 grid(xcd_grid(nwaves)), block(64);
-  if (c.L <= 16)
-    delta_flush_kernel<ST, 16, DK><<<grid, block, 0, st>>>(c, slot_idx, num_fold, parts, nwaves);
-  else
-    delta_flush_kernel<ST, 32, DK><<<grid, block, 0, st>>>(c, slot_idx, num_fold, parts, nwaves);
+template <int ST, int KW, int DK>
+hipError_t delta_flush_kw(const DCache &c, const int32_t *slot_idx, const int32_t *num_fold, int n, hipStream_t st) {
+  const int share = wave_share<ST, DK>((int64_t)n * c.Hv, c.dv / 16), parts = (c.dv / 16 + share - 1) / share;
+  const int nwaves = n * c.Hv * parts;
+  delta_flush_kernel<ST, KW, DK><<<dim3(xcd_grid(nwaves)), dim3(64), window_lds<KW>(c.dv), st>>>(c, slot_idx, num_fold, parts, share, nwaves);
   const hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;
   delta_ring_advance_kernel<ST><<<dim3((unsigned)((n + 255) / 256)), dim3(256), 0, st>>>(c, slot_idx, num_fold, n);
@@ -570,8 +689,8 @@ hipError_t delta_flush_dk(const DCache &c, const int32_t *slot_idx, const int32_
 
 template <int ST>
 hipError_t delta_flush_st(const DCache &c, const int32_t *slot_idx, const int32_t *num_fold, int n, hipStream_t st) {
-  return c.dk == 64 ? delta_flush_dk<ST, 64>(c, slot_idx, num_fold, n, st)
-                    : delta_flush_dk<ST, 128>(c, slot_idx, num_fold, n, st);
+  if (c.dk == 64) return c.L <= 16 ? delta_flush_kw<ST, 16, 64>(c, slot_idx, num_fold, n, st) : delta_flush_kw<ST, 32, 64>(c, slot_idx, num_fold, n, st);
+  return c.L <= 16 ? delta_flush_kw<ST, 16, 128>(c, slot_idx, num_fold, n, st) : delta_flush_kw<ST, 32, 128>(c, slot_idx, num_fold, n, st);
 }
 
 template <int ST, bool READ>

@@ -18,12 +18,12 @@ int check_sizes(int32_t batch, int32_t vocab) {
   if (batch > 65535) return api_fail(SSU_ERR_UNSUPPORTED, "batch %d exceeds 65535 entries per call", batch);
   if (vocab < 1) return api_fail(SSU_ERR_INVALID, "vocab must be positive (got %d)", vocab);
   if (vocab > (1 << 24)) return api_fail(SSU_ERR_UNSUPPORTED, "vocab %d exceeds 2^24", vocab);
-  if ((int64_t)batch * ssu::verify_segments(vocab) > (1 << 23))
-    return api_fail(SSU_ERR_UNSUPPORTED, "batch %d x vocab %d exceeds 2^23 pieces of %d values per call", batch, vocab, ssu::kVerifySeg);
+  if ((int64_t)batch * ((vocab + 4095) / 4096) > (1 << 23))
+    return api_fail(SSU_ERR_UNSUPPORTED, "batch %d x vocab %d exceeds 2^23 pieces of 4096 values per call", batch, vocab);
   return SSU_OK;
 }
 
-size_t bytes_for(int64_t batch, int32_t vocab) { return (size_t)(batch * ssu::verify_segments(vocab)) * sizeof(double); }
+size_t bytes_for(int64_t batch, int32_t vocab) { return (size_t)(batch * ssu::verify_words(vocab)) * sizeof(double); }
 
 }  // namespace
 

@@ -12,10 +12,12 @@ namespace ssu {
 
 enum ProbType { kPF32 = 0, kPBF16 = 1, kPF16 = 2 };
 
-constexpr int kVerifySeg = 4096;      // values of a row per workgroup of the first kernel
+constexpr int kVerifyPiece = 1024;    // values of a row whose sum is kept: 16 a lane
 constexpr int kVerifyMaxTokens = 64;  // the drafts of an entry are tested by the lanes of one wave
 
-inline int verify_segments(int vocab) { return (vocab + kVerifySeg - 1) / kVerifySeg; }
+inline int verify_pieces(int vocab) { return (vocab + kVerifyPiece - 1) / kVerifyPiece; }
+// 8-byte words of scratch of an entry: the pieces' sums, then the verdict
+inline int verify_words(int vocab) { return verify_pieces(vocab) + 2; }
 
 struct KVerify {
   int batch, T, vocab, ring_len, reserve;
@@ -27,7 +29,7 @@ struct KVerify {
   int32_t *out, *accepted;
   const int32_t *live, *fold;
   int32_t *next_live, *next_fold, *next_left;
-  double *ws;                    // [batch][segments]
+  double *ws;                    // [batch][verify_words]
   int32_t *status;
   int wide;                      // rows can be read 16 bytes at a time
 };

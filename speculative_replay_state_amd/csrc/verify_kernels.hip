@@ -1,12 +1,17 @@
 // Verification of drafted tokens (ssu_verify).
 //
-// Two kernels.  verify_sum_kernel, a workgroup per (entry, segment of the
-// vocabulary): the number n of accepted drafts (one lane per draft, a
-// ballot), then the segment's sum of the residual r of row n in fp64.
-// verify_pick_kernel, a workgroup per entry: the segment in which the running
-// sum passes u' sum r, the first value in it that does, and the bookkeeping.
-// What bounds them is one read of row n of both distributions; the second
-// kernel reads one segment of it again.
+// Two kernels.  verify_sum_kernel, a wave per (entry, piece of 1024 values of
+// the vocabulary): the number n of accepted drafts (one lane per draft, a
+// ballot), then the sum of the residual r of row n over the piece, in fp64.
+// verify_pick_kernel, a wave per entry: the piece in which the running sum
+// passes u' sum r, the first value in it that does, and the bookkeeping.
+//
+// What bounds them is one read of row n of both distributions, behind the
+// drafts' own (dependent) reads.  256 entries of 8 tokens, 131072 bf16 values in
+// two distributions: 32.4 us, 4.15 TB/s; 64 entries, 100003 fp32 values without
+// draft probabilities (rows no 16 bytes apart): 13.1 us; one entry of 32000:
+// 8.9 us.  With four pieces a wave 36.7, 14.9 and 10.5 us (fewer waves wait for
+// their drafts); with the verdicts in a kernel of their own 31.6, 15.2, 11.9.
 #include "ssu_device.cuh"
 #include "verify_internal.h"
 
@@ -16,9 +21,7 @@ namespace ssu {
 
 namespace {
 
-constexpr int kT = 256;                       // threads of a workgroup
-constexpr int kPer = kVerifySeg / kT;         // values of a segment per thread
-constexpr int kWavesV = kT / 64;
+constexpr int kLane = kVerifyPiece / 64;  // values of a piece per lane
 
 template <int PT>
 __device__ __forceinline__ float prob_at(const uint8_t *row, int i) {
@@ -28,30 +31,21 @@ __device__ __forceinline__ float prob_at(const uint8_t *row, int i) {
   return (float)__builtin_bit_cast(_Float16, v);
 }
 
-// 8 values from index i (a multiple of 8) on; 0 past the vocabulary.
+// Eight neighbouring values as they are in memory, from 16-byte aligned pieces.
 template <int PT>
-__device__ __forceinline__ void probs8(const uint8_t *row, int i, int vocab, int wide, float (&x)[8]) {
-  if (wide && i + 8 <= vocab) {
-    if constexpr (PT == kPF32) {
-      const f32x4 a = *reinterpret_cast<const f32x4 *>(row + (int64_t)i * 4), b = *reinterpret_cast<const f32x4 *>(row + (int64_t)i * 4 + 16);
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        x[r] = a[r];
-        x[4 + r] = b[r];
-      }
-    } else {
-      const u32x4 v = ld16(row + (int64_t)i * 2);
-#pragma unroll
-      for (int r = 0; r < 8; ++r) {
-        const uint16_t w = (uint16_t)(v[r / 2] >> (16 * (r & 1)));
-        x[r] = PT == kPBF16 ? bf2f(w) : (float)__builtin_bit_cast(_Float16, w);
-      }
-    }
-  } else {
-#pragma unroll
-    for (int r = 0; r < 8; ++r) x[r] = i + r < vocab ? prob_at<PT>(row, i + r) : 0.f;
+struct Eight {
+  u32x4 w[PT == kPF32 ? 2 : 1];
+  __device__ __forceinline__ void load(const uint8_t *row, int i) {
+    const uint8_t *at = row + (int64_t)i * (PT == kPF32 ? 4 : 2);
+    w[0] = ld16(at);
+    if constexpr (PT == kPF32) w[1] = ld16(at + 16);
   }
-}
+  __device__ __forceinline__ float value(int k) const {
+    if constexpr (PT == kPF32) return __uint_as_float(w[k / 4][k % 4]);
+    const uint16_t h = (uint16_t)(w[0][k / 2] >> (16 * (k & 1)));
+    return PT == kPBF16 ? bf2f(h) : (float)__builtin_bit_cast(_Float16, h);
+  }
+};
 
 struct Verdict {
   int bos, T;   // T < 0: the entry's lengths are not what they have to be
@@ -98,25 +92,7 @@ __device__ __forceinline__ Verdict verdict(const KVerify &v, int b, int lane) {
   return o;
 }
 
-// r of values i .. i + 7 of row n
-template <int PT>
-__device__ __forceinline__ void residual8(const KVerify &v, const Verdict &o, bool rejected, int i, float (&r)[8]) {
-  const int64_t row = (int64_t)o.bos + o.n;
-  probs8<PT>(v.p + row * v.p_stride, i, v.vocab, v.wide, r);
-  if (rejected) {
-    if (v.q) {
-      float q[8];
-      probs8<PT>(v.q + row * v.q_stride, i, v.vocab, v.wide, q);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) r[k] -= q[k];
-    } else {
-#pragma unroll
-      for (int k = 0; k < 8; ++k) r[k] -= i + k == o.draft ? 1.f : 0.f;
-    }
-  }
-#pragma unroll
-  for (int k = 0; k < 8; ++k) r[k] = r[k] > 0.f ? r[k] : 0.f;  // NaN: 0
-}
+__device__ __forceinline__ float positive(float x) { return x > 0.f ? x : 0.f; }  // NaN: 0
 
 __device__ __forceinline__ double wave_sum(double x) {
 #pragma unroll
@@ -124,169 +100,180 @@ __device__ __forceinline__ double wave_sum(double x) {
   return x;
 }
 
-template <int PT>
-__global__ __launch_bounds__(kT) void verify_sum_kernel(KVerify v) {
-  __shared__ double part[kWavesV];
-  const int tid = threadIdx.x, lane = tid & 63, b = blockIdx.y, seg = blockIdx.x;
-  const Verdict o = verdict<PT>(v, b, lane);
-  if (o.T <= 0) return;
+// Sum of r over a piece, in every lane, with every load in flight before the
+// first is used.  WIDE (rows of 16-byte pieces, this one within the
+// vocabulary): 8 neighbours a lane and load; else a value a lane, 64 neighbours
+// a load, and past the vocabulary its last value, not counted.
+template <int PT, bool WIDE>
+__device__ __forceinline__ double piece_sum(const KVerify &v, const Verdict &o, bool rejected, int piece, int lane) {
+  const int64_t row = (int64_t)o.bos + o.n;
+  const bool less = rejected && v.q;  // (without: p is read again, from the cache, and not used)
+  const uint8_t *p = v.p + row * v.p_stride, *q = less ? v.q + row * v.q_stride : p;
+  const int i0 = piece * kVerifyPiece;
   double sum = 0.0;
+  auto add = [&](float a, float b, int i) {
+    if (rejected) a -= less ? b : (i == o.draft ? 1.f : 0.f);
+    sum += (double)(WIDE || i < v.vocab ? positive(a) : 0.f);
+  };
+  if constexpr (WIDE) {
+    Eight<PT> a[kLane / 8], b[kLane / 8];
 #pragma unroll
-  for (int k = 0; k < kPer / 8; ++k) {
-    float r[8];
-    residual8<PT>(v, o, o.n < o.T - 1 && o.draft >= 0, seg * kVerifySeg + (k * kT + tid) * 8, r);
+    for (int k = 0; k < kLane / 8; ++k) {
+      a[k].load(p, i0 + k * 512 + lane * 8);
+      b[k].load(q, i0 + k * 512 + lane * 8);
+    }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) sum += (double)r[i];
+    for (int k = 0; k < kLane / 8; ++k)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) add(a[k].value(e), b[k].value(e), i0 + k * 512 + lane * 8 + e);
+  } else {
+    float a[kLane], b[kLane];
+#pragma unroll
+    for (int k = 0; k < kLane; ++k) {
+      const int i = min(i0 + k * 64 + lane, v.vocab - 1);
+      a[k] = prob_at<PT>(p, i);
+      b[k] = prob_at<PT>(q, i);
+    }
+#pragma unroll
+    for (int k = 0; k < kLane; ++k) add(a[k], b[k], i0 + k * 64 + lane);
   }
-  sum = wave_sum(sum);
-  if (lane == 0) part[tid >> 6] = sum;
-  __syncthreads();
-  if (tid == 0) v.ws[(int64_t)b * gridDim.x + seg] = part[0] + part[1] + part[2] + part[3];
+  return wave_sum(sum);
 }
 
-// Sums of the threads before this one, and of all, over the workgroup.
-__device__ __forceinline__ double block_scan(double x, int tid, double *part, double *total) {
-  const int lane = tid & 63, wave = tid >> 6;
-  double s = x;
+constexpr int kSumWaves = 4;
+
+// The verdict of an entry in its words of the scratch.
+__device__ __forceinline__ Verdict read_verdict(const KVerify &v, const double *ws, int pieces, int b) {
+  const int2 w0 = *reinterpret_cast<const int2 *>(ws + pieces), w1 = *reinterpret_cast<const int2 *>(ws + pieces + 1);
+  Verdict o;
+  o.bos = v.cu ? v.cu[b] : b * v.T;
+  o.n = w0.x;
+  o.draft = w0.y;
+  o.bits = w1.x;
+  o.T = w1.y;
+  return o;
+}
+__device__ __forceinline__ void write_verdict(const Verdict &o, double *ws, int pieces) {
+  *reinterpret_cast<int2 *>(ws + pieces) = int2{o.n, o.draft};
+  *reinterpret_cast<int2 *>(ws + pieces + 1) = int2{o.bits, o.T};
+}
+
+template <int PT>
+__global__ __launch_bounds__(kSumWaves * 64) void verify_sum_kernel(KVerify v, int pieces) {
+  const int lane = threadIdx.x & 63, b = blockIdx.y, piece = blockIdx.x * kSumWaves + (threadIdx.x >> 6);
+  if (piece >= pieces) return;
+  double *ws = v.ws + (int64_t)b * (pieces + 2);
+  const Verdict o = verdict<PT>(v, b, lane);
+  if (piece == 0 && lane == 0) write_verdict(o, ws, pieces);
+  if (o.T <= 0) return;
+  const bool rejected = o.n < o.T - 1 && o.draft >= 0;
+  const double sum = v.wide && (piece + 1) * kVerifyPiece <= v.vocab ? piece_sum<PT, true>(v, o, rejected, piece, lane)
+                                                                     : piece_sum<PT, false>(v, o, rejected, piece, lane);
+  if (lane == 0) ws[piece] = sum;
+}
+
+// Sums of the lanes up to and with this one.
+__device__ __forceinline__ double wave_scan(double x, int lane) {
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
-    const double y = __shfl_up(s, d);
-    if (lane >= d) s += y;
+    const double y = __shfl_up(x, d);
+    if (lane >= d) x += y;
   }
-  __syncthreads();  // `part` may still be read from the scan before
-  if (lane == 63) part[wave] = s;
-  __syncthreads();
-  double before = 0.0, all = 0.0;
-#pragma unroll
-  for (int w = 0; w < kWavesV; ++w) {
-    if (w < wave) before += part[w];
-    all += part[w];
-  }
-  *total = all;
-  return before + (s - x);
-}
-
-// The smallest (SMALL) or largest of the threads' values.
-template <bool SMALL>
-__device__ __forceinline__ int block_pick(int x, int tid, int *part) {
-#pragma unroll
-  for (int s = 32; s > 0; s >>= 1) {
-    const int y = __shfl_xor(x, s);
-    x = SMALL ? min(x, y) : max(x, y);
-  }
-  __syncthreads();
-  if ((tid & 63) == 0) part[tid >> 6] = x;
-  __syncthreads();
-  x = part[0];
-#pragma unroll
-  for (int w = 1; w < kWavesV; ++w) x = SMALL ? min(x, part[w]) : max(x, part[w]);
   return x;
 }
 
-// Sum of r over the row, from scratch (only where the residual is empty).
-template <int PT>
-__device__ double row_mass(const KVerify &v, const Verdict &o, int tid, double *part, double *seg_sum, int nseg) {
-  for (int s = 0; s < nseg; ++s) {
-    double x = 0.0, all;
-    for (int k = 0; k < kPer / 8; ++k) {
-      float r[8];
-      residual8<PT>(v, o, false, s * kVerifySeg + (k * kT + tid) * 8, r);
-      for (int i = 0; i < 8; ++i) x += (double)r[i];
-    }
-    block_scan(x, tid, part, &all);
-    if (tid == 0) seg_sum[s] = all;
-  }
-  __threadfence_block();
-  __syncthreads();
-  double sum = 0.0;
-  for (int s = tid; s < nseg; s += kT) sum += seg_sum[s];
-  double all;
-  block_scan(sum, tid, part, &all);
-  return all;
-}
+// A sum that this kernel may have written itself: past the CU's own cache.
+__device__ __forceinline__ double kept_sum(const double *p) { return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
+
+__device__ __forceinline__ int first_lane(uint64_t set) { return (int)__builtin_ctzll(set); }
+__device__ __forceinline__ int last_lane(uint64_t set) { return 63 - (int)__builtin_clzll(set); }
 
 template <int PT>
-__global__ __launch_bounds__(kT) void verify_pick_kernel(KVerify v, int nseg) {
-  __shared__ double part[kWavesV];
-  __shared__ int ipart[kWavesV];
-  __shared__ double s_before;
-  __shared__ int s_seg;
-  const int tid = threadIdx.x, lane = tid & 63, b = blockIdx.x;
-  const Verdict o = verdict<PT>(v, b, lane);
+__global__ __launch_bounds__(64) void verify_pick_kernel(KVerify v, int pieces) {
+  const int lane = threadIdx.x, b = blockIdx.x;
+  double *sums = v.ws + (int64_t)b * (pieces + 2);
+  const Verdict o = read_verdict(v, sums, pieces, b);
   int bits = o.bits, token = -1;
   if (o.T > 0) {
-    double *sums = v.ws + (int64_t)b * nseg;
     bool rejected = o.n < o.T - 1 && o.draft >= 0;
-    double x = 0.0, total;
-    for (int s = tid; s < nseg; s += kT) x += sums[s];
-    block_scan(x, tid, part, &total);
-    if (!(total > 0.0) && rejected) {
+    // each lane a run of neighbouring pieces
+    const int per = (pieces + 63) / 64, p0 = lane * per, p1 = min(p0 + per, pieces);
+    double x = 0.0;
+    for (int k = p0; k < p1; ++k) x += sums[k];
+    double upto = wave_scan(x, lane), total = __shfl(upto, 63);
+    if (!(total > 0.0) && rejected) {  // an empty residual: the row itself
       rejected = false;
-      total = row_mass<PT>(v, o, tid, part, sums, nseg);
+      for (int k = 0; k < pieces; ++k) {
+        const double y = piece_sum<PT, false>(v, o, false, k, lane);
+        if (lane == 0) __hip_atomic_store(sums + k, y, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      }
+      __threadfence();
+      x = 0.0;
+      for (int k = p0; k < p1; ++k) x += kept_sum(sums + k);
+      upto = wave_scan(x, lane);
+      total = __shfl(upto, 63);
     }
     if (!(total > 0.0) || total > 1.7e308) {
       bits |= SSU_STATUS_BAD_PROBS;
     } else {
       const float uf = v.uf[b];
       const double want = (double)(uf > 0.f ? uf : 0.f) * total;
-      // the first segment whose running sum passes `want`, else the last with mass
-      if (tid == 0) s_seg = -1;
-      int found = nseg;
-      double base = 0.0;
-      for (int s0 = 0; s0 < nseg && found == nseg; s0 += kT) {
-        const int s = s0 + tid;
-        const double y = s < nseg ? sums[s] : 0.0;
-        double all;
-        const double before = base + block_scan(y, tid, part, &all);
-        found = block_pick<true>(y > 0.0 && before + y > want ? s : nseg, tid, ipart);
-        const int l = block_pick<false>(y > 0.0 ? s : -1, tid, ipart);
-        if (s == (found < nseg ? found : l) && y > 0.0) {
-          s_seg = s;
-          s_before = before;
+      // the run, then the piece in it, whose running sum passes `want`; where
+      // rounding leaves none, the last with mass
+      const uint64_t over = __ballot(x > 0.0 && upto > want), some = __ballot(x > 0.0);
+      const int run = over ? first_lane(over) : last_lane(some);
+      int piece = -1;
+      double before = upto - x, at = 0.0;  // (in lane `run`)
+      for (int k = p0; k < p1; ++k) {
+        const double y = kept_sum(sums + k);
+        if (y > 0.0) {
+          piece = k;
+          at = before;
+          if (before + y > want) break;
         }
-        base += all;
+        before += y;
       }
-      __syncthreads();
-      const int seg = s_seg;
-      const double start = s_before;
-      // values in order: thread t holds 16 neighbours
-      float r[kPer];
-      double sum = 0.0;
+      piece = __shfl(piece, run);
+      at = __shfl(at, run);
+      // 16 neighbours a lane
+      const int64_t row = (int64_t)o.bos + o.n;
+      const uint8_t *p = v.p + row * v.p_stride, *q = rejected && v.q ? v.q + row * v.q_stride : p;
+      const int i0 = piece * kVerifyPiece + lane * kLane;
+      float r[kLane], less[kLane];
 #pragma unroll
-      for (int k = 0; k < kPer / 8; ++k) {
-        float y[8];
-        residual8<PT>(v, o, rejected, seg * kVerifySeg + tid * kPer + k * 8, y);
+      for (int i = 0; i < kLane; ++i) r[i] = prob_at<PT>(p, min(i0 + i, v.vocab - 1));
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          r[8 * k + i] = y[i];
-          sum += (double)y[i];
-        }
+      for (int i = 0; i < kLane; ++i) less[i] = prob_at<PT>(q, min(i0 + i, v.vocab - 1));
+      double mine = 0.0;
+#pragma unroll
+      for (int i = 0; i < kLane; ++i) {
+        if (rejected) r[i] -= q != p ? less[i] : (i0 + i == o.draft ? 1.f : 0.f);
+        r[i] = i0 + i < v.vocab ? positive(r[i]) : 0.f;
+        mine += (double)r[i];
       }
-      double all;
-      double run = start + block_scan(sum, tid, part, &all);
-      int hit = v.vocab, end = -1;
+      double sum = at + (wave_scan(mine, lane) - mine);
+      int hit = -1, end = -1;
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        const int at = seg * kVerifySeg + tid * kPer + i;
-        run += (double)r[i];
+      for (int i = 0; i < kLane; ++i) {
+        sum += (double)r[i];
         if (r[i] > 0.f) {
-          end = at;
-          if (run > want && hit == v.vocab) hit = at;
+          end = i;
+          if (hit < 0 && sum > want) hit = i;
         }
       }
-      hit = block_pick<true>(hit, tid, ipart);
-      end = block_pick<false>(end, tid, ipart);
-      token = hit < v.vocab ? hit : end;
+      const uint64_t hits = __ballot(hit >= 0), ends = __ballot(end >= 0);
+      const int from = hits ? first_lane(hits) : last_lane(ends);
+      token = piece * kVerifyPiece + from * kLane + __shfl(hits ? hit : end, from);
     }
   }
   const int kept = o.T > 0 ? o.n + 1 : 0;
-  if (tid < v.T) {
+  if (lane < v.T) {
     int w = -1;
-    if (tid + 1 < kept) w = v.tokens[(int64_t)o.bos + tid + 1];
-    if (tid + 1 == kept) w = token;
-    v.out[(int64_t)b * v.T + tid] = w;
+    if (lane + 1 < kept) w = v.tokens[(int64_t)o.bos + lane + 1];
+    if (lane + 1 == kept) w = token;
+    v.out[(int64_t)b * v.T + lane] = w;
   }
-  if (tid == 0) {
+  if (lane == 0) {
     v.accepted[b] = kept;
     if (v.next_live) {
       const int left = v.live[b] - (v.fold ? v.fold[b] : 0) + kept;
@@ -301,11 +288,12 @@ __global__ __launch_bounds__(kT) void verify_pick_kernel(KVerify v, int nseg) {
 
 template <int PT>
 hipError_t verify_pt(const KVerify &v, hipStream_t st) {
-  const int nseg = verify_segments(v.vocab);
-  verify_sum_kernel<PT><<<dim3((unsigned)nseg, (unsigned)v.batch), dim3(kT), 0, st>>>(v);
+  const int pieces = verify_pieces(v.vocab);
+  const dim3 grid((unsigned)((pieces + kSumWaves - 1) / kSumWaves), (unsigned)v.batch);
+  verify_sum_kernel<PT><<<grid, dim3(kSumWaves * 64), 0, st>>>(v, pieces);
   const hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;
-  verify_pick_kernel<PT><<<dim3((unsigned)v.batch), dim3(kT), 0, st>>>(v, nseg);
+  verify_pick_kernel<PT><<<dim3((unsigned)v.batch), dim3(64), 0, st>>>(v, pieces);
   return hipGetLastError();
 }
 

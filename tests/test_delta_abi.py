@@ -87,6 +87,7 @@ def _prefill(**kw):
     (dict(dim_v=8), -2, "dim_v"),
     (dict(dim_v=24), -2, "dim_v"),
     (dict(dim_v=272), -2, "dim_v"),
+    (dict(nheads_v=1 << 16), -2, "2^23"),
     (dict(ring_len=0), -2, "ring_len"),
     (dict(ring_len=33), -2, "ring_len"),
     (dict(state_dtype=ssu.SSU_FP8_E4M3), -2, "state_dtype"),
@@ -164,7 +165,7 @@ def test_state_stride_refusals(stride, read, msg):
     (dict(k=None), -1, "NULL"),
     (dict(k_row_stride=128), -1, "k_row_stride"),
     (dict(q_row_stride=1 << 23), -2, "2^23"),
-    (dict(nheads_v=1 << 16, rows=0, num_seqs=1, v_row_stride=1 << 23), -2, "2^23"),
+    (dict(nheads_v=1 << 16, rows=0, num_seqs=1), -2, "2^23"),
     (dict(workspace=None), -4, "workspace"),
     (dict(workspace_bytes=64), -4, "workspace"),
     (dict(workspace=FAKE + 4), -1, "workspace"),
@@ -220,7 +221,7 @@ def test_verify_refusals(kw, code, msg):
 
 def test_verify_no_op_and_workspace():
     assert verification.ssu_verify(_verify(batch=0, tokens=None)) == 0
-    assert ssu.verify_workspace_size(3, 4096) == 3 * 8 and ssu.verify_workspace_size(3, 4097) == 2 * 3 * 8
+    assert ssu.verify_workspace_size(3, 4096) == 3 * (4 + 2) * 8 and ssu.verify_workspace_size(3, 4097) == 3 * (5 + 2) * 8
     assert ssu.verify_workspace_size(-1, 5) == 0
 
 
