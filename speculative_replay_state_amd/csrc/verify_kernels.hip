@@ -5,13 +5,16 @@
 // ballot), then the sum of the residual r of row n over the piece, in fp64.
 // verify_pick_kernel, a wave per entry: the piece in which the running sum
 // passes u' sum r, the first value in it that does, and the bookkeeping.
+// verify_row_kernel does both for an entry in one workgroup, where rows are
+// short or the entries many.
 //
 // What bounds them is one read of row n of both distributions, behind the
 // drafts' own (dependent) reads.  256 entries of 8 tokens, 131072 bf16 values in
-// two distributions: 32.4 us, 4.15 TB/s; 64 entries, 100003 fp32 values without
-// draft probabilities (rows no 16 bytes apart): 13.1 us; one entry of 32000:
-// 8.9 us.  With four pieces a wave 36.7, 14.9 and 10.5 us (fewer waves wait for
-// their drafts); with the verdicts in a kernel of their own 31.6, 15.2, 11.9.
+// two distributions: 27.9 us, 4.8 TB/s (32.1 in two launches); 64 entries,
+// 100003 fp32 values without draft probabilities (rows no 16 bytes apart):
+// 13.1 us; one entry of 32000: 8.7 us.  With four pieces a wave of verify_sum_kernel 36.7, 14.9 and
+// 10.5 us, with one 32.4, 13.1 and 8.9 (fewer waves wait for their drafts);
+// with the verdicts in a kernel of their own 31.6, 15.2, 11.9.
 #include "ssu_device.cuh"
 #include "verify_internal.h"
 
@@ -140,7 +143,8 @@ __device__ __forceinline__ double piece_sum(const KVerify &v, const Verdict &o, 
   return wave_sum(sum);
 }
 
-constexpr int kSumWaves = 4;
+constexpr int kSumWaves = 4;                     // waves of a workgroup of verify_sum_kernel
+constexpr int kRowWaves = 16, kRowPieces = 256;  // of verify_row_kernel; the pieces its LDS holds
 
 // The verdict of an entry in its words of the scratch.
 __device__ __forceinline__ Verdict read_verdict(const KVerify &v, const double *ws, int pieces, int b) {
@@ -182,34 +186,39 @@ __device__ __forceinline__ double wave_scan(double x, int lane) {
   return x;
 }
 
-// A sum that this kernel may have written itself: past the CU's own cache.
-__device__ __forceinline__ double kept_sum(const double *p) { return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
-
 __device__ __forceinline__ int first_lane(uint64_t set) { return (int)__builtin_ctzll(set); }
 __device__ __forceinline__ int last_lane(uint64_t set) { return 63 - (int)__builtin_clzll(set); }
 
-template <int PT>
-__global__ __launch_bounds__(64) void verify_pick_kernel(KVerify v, int pieces) {
-  const int lane = threadIdx.x, b = blockIdx.x;
-  double *sums = v.ws + (int64_t)b * (pieces + 2);
-  const Verdict o = read_verdict(v, sums, pieces, b);
+// One wave's pick for entry b from the pieces' sums: in LDS, or in memory, where
+// it reads past its CU's own cache what it may have written itself.
+template <int PT, bool LDS>
+__device__ __forceinline__ void pick(const KVerify &v, const Verdict &o, double *sums, int pieces, int b, int lane) {
+  auto kept_sum = [&](int k) { return LDS ? sums[k] : __hip_atomic_load(sums + k, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); };
   int bits = o.bits, token = -1;
   if (o.T > 0) {
     bool rejected = o.n < o.T - 1 && o.draft >= 0;
     // each lane a run of neighbouring pieces
     const int per = (pieces + 63) / 64, p0 = lane * per, p1 = min(p0 + per, pieces);
     double x = 0.0;
-    for (int k = p0; k < p1; ++k) x += sums[k];
+    for (int k = p0; k < p1; ++k) x += kept_sum(k);
     double upto = wave_scan(x, lane), total = __shfl(upto, 63);
     if (!(total > 0.0) && rejected) {  // an empty residual: the row itself
       rejected = false;
       for (int k = 0; k < pieces; ++k) {
         const double y = piece_sum<PT, false>(v, o, false, k, lane);
-        if (lane == 0) __hip_atomic_store(sums + k, y, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        if (lane == 0) {
+          if (LDS)
+            sums[k] = y;
+          else
+            __hip_atomic_store(sums + k, y, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        }
       }
-      __threadfence();
+      if (LDS)
+        wave_sync();
+      else
+        __threadfence();
       x = 0.0;
-      for (int k = p0; k < p1; ++k) x += kept_sum(sums + k);
+      for (int k = p0; k < p1; ++k) x += kept_sum(k);
       upto = wave_scan(x, lane);
       total = __shfl(upto, 63);
     }
@@ -225,7 +234,7 @@ __global__ __launch_bounds__(64) void verify_pick_kernel(KVerify v, int pieces) 
       int piece = -1;
       double before = upto - x, at = 0.0;  // (in lane `run`)
       for (int k = p0; k < p1; ++k) {
-        const double y = kept_sum(sums + k);
+        const double y = kept_sum(k);
         if (y > 0.0) {
           piece = k;
           at = before;
@@ -287,8 +296,44 @@ __global__ __launch_bounds__(64) void verify_pick_kernel(KVerify v, int pieces) 
 }
 
 template <int PT>
+__global__ __launch_bounds__(64) void verify_pick_kernel(KVerify v, int pieces) {
+  const int b = blockIdx.x;
+  double *ws = v.ws + (int64_t)b * (pieces + 2);
+  pick<PT, false>(v, read_verdict(v, ws, pieces, b), ws, pieces, b, threadIdx.x);
+}
+
+// Both at once: a workgroup per entry, its sums in LDS; every wave forms the
+// verdict for itself.  At most kRowPieces pieces (the launch sees to it).
+template <int PT>
+__global__ __launch_bounds__(kRowWaves * 64) void verify_row_kernel(KVerify v, int pieces) {
+  __shared__ double sums[kRowPieces];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, b = blockIdx.x;
+  const Verdict o = verdict<PT>(v, b, lane);
+  if (o.T > 0) {
+    const bool rejected = o.n < o.T - 1 && o.draft >= 0;
+    for (int k = wave; k < pieces; k += kRowWaves) {
+      const double sum = v.wide && (k + 1) * kVerifyPiece <= v.vocab ? piece_sum<PT, true>(v, o, rejected, k, lane)
+                                                                     : piece_sum<PT, false>(v, o, rejected, k, lane);
+      if (lane == 0) sums[k] = sum;
+    }
+  }
+  __syncthreads();
+  if (wave == 0) pick<PT, true>(v, o, sums, pieces, b, lane);
+}
+
+template <int PT>
 hipError_t verify_pt(const KVerify &v, hipStream_t st) {
   const int pieces = verify_pieces(v.vocab);
+  // One launch for short rows (one entry of 4096 values 7.6 us against 10.5, of
+  // 40000 bf16 values 10.0 against 10.8, of 65536 12.0 against 10.1), and for
+  // entries that fill the card by themselves where the values have two bytes (192
+  // rows of 131072 bf16 values 23.0 us against 24.0, 512 48.3 against 55.8; 128
+  // rows 22.1 against 18.9; 512 fp32 rows without draft probabilities 60.1
+  // against 55.9).
+  if (pieces <= 40 || (v.batch >= 192 && PT != kPF32 && pieces <= kRowPieces)) {
+    verify_row_kernel<PT><<<dim3((unsigned)v.batch), dim3(kRowWaves * 64), 0, st>>>(v, pieces);
+    return hipGetLastError();
+  }
   const dim3 grid((unsigned)((pieces + kSumWaves - 1) / kSumWaves), (unsigned)v.batch);
   verify_sum_kernel<PT><<<grid, dim3(kSumWaves * 64), 0, st>>>(v, pieces);
   const hipError_t err = hipGetLastError();

@@ -107,6 +107,8 @@ CASES = [  # batch, T, vocab, dtype, draft probabilities, row stride - vocab (0:
     (1, 1, 1, "f32", True, 0), (3, 4, 2, "f32", True, 0), (5, 4, 7, "bf16", False, 0), (4, 5, 1000, "f32", True, 24),
     (7, 3, 4095, "f16", True, 1), (7, 3, 4096, "f32", False, 0), (7, 3, 4097, "bf16", True, 0), (2, 64, 300, "f32", True, 0),
     (40, 8, 9001, "f32", True, 3), (3, 2, 100003, "bf16", False, 0), (33, 2, 12288, "f16", True, 8),
+    # the two launches and the one at their border, entries that fill the card
+    (5, 3, 40960, "f32", True, 0), (5, 3, 40961, "f32", False, 0), (195, 2, 41000, "bf16", True, 0), (195, 2, 41003, "f16", False, 1),
 ]
 
 
@@ -171,6 +173,18 @@ def test_rows_without_mass():
     for uf, want in ((-3.0, 1), (nan, 1), (1.0, 3), (7.0, 3)):
         out, _, _ = run([2], np.array([[0, 0.2, 0, 0.8, 0]], np.float32), None, [0.0], [uf], 1)
         assert out.tolist() == [[want]], uf
+
+
+@pytest.mark.parametrize("vocab", [3000, 50000])
+def test_an_empty_residual_draws_from_the_row(vocab):
+    """p = q and a draft that neither gives anything: every piece is summed again, in one launch and in two."""
+    rng = np.random.default_rng(6)
+    p = draw(rng, 8, vocab)
+    p[:, 17] = 0.0
+    uf = np.float32([0.0, 0.3, 0.7, 0.9999])
+    out, acc, status = run([5, 17] * 4, p, p, [0.5] * 8, uf, 2)
+    want, count, bits = reference([5, 17] * 4, p.astype(np.float64), p.astype(np.float64), [0.5] * 8, uf, np.arange(0, 9, 2), 2, vocab)
+    assert np.array_equal(out, want) and np.array_equal(acc, count) and status == bits == 0
 
 
 def test_tokens_outside_the_vocabulary():
