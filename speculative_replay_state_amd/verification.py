@@ -54,7 +54,9 @@ def _probs(t, name: str, rows: int, vocab: int) -> int:
     _shape(t, name, (rows, vocab))
     if vocab > 1 and t.stride(1) != 1:
         raise ValueError("%s: each row must be contiguous" % name)
-    return max(t.stride(0), vocab) if rows > 1 else vocab
+    if rows > 1 and t.stride(0) < vocab:
+        raise ValueError("%s: its rows overlap (%d elements apart, of %d)" % (name, t.stride(0), vocab))
+    return t.stride(0) if rows > 1 else vocab
 
 
 def make_verify(tokens, target_probs, draft_probs, u, u_final, out_tokens, num_accepted, workspace, cu_seqlens=None,

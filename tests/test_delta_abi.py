@@ -234,3 +234,15 @@ def test_front_end_refuses_host_tensors():
         ssu.make_delta_prefill(z(2, dt=torch.int32), z(4, 1, 64), z(4, 1, 64), z(4, 1, 64), z(4, 1), z(4, 1), z(1), z(1), z(4, 1, 64))
     with pytest.raises(ValueError, match="device tensor"):
         ssu.make_verify(z(4, dt=torch.int32), z(4, 9), None, z(4), z(1), z(1, 4, dt=torch.int32), z(1, dt=torch.int32), z(8))
+
+
+def test_expanded_probability_rows_are_refused(monkeypatch):
+    """One row expanded over several has no distance between rows; only a single row needs none."""
+    import torch
+    from speculative_replay_state_amd import verification as V
+    monkeypatch.setattr(V, "_on_device", lambda t, name: None)
+    row = torch.zeros(1, 10)
+    assert V._probs(row, "p", 1, 10) == 10 and V._probs(torch.zeros(3, 16)[:, :10], "p", 3, 10) == 16
+    for t in (row.expand(3, -1), torch.zeros(40).as_strided((3, 10), (4, 1))):
+        with pytest.raises(ValueError, match="target_probs: its rows overlap"):
+            V._probs(t, "target_probs", 3, 10)
