@@ -87,14 +87,14 @@ __device__ __forceinline__ DEntry delta_entry(const DCache &c, const DStep &s, i
   asm volatile("" : "+s"(w0), "+s"(w1), "+s"(slot), "+s"(pn));
   DEntry e;
   e.bos = s.cu ? w0 : b * s.T;
-  e.T = s.cu ? w1 - w0 : s.T;
+  e.T = s.cu ? (int)((uint32_t)w1 - (uint32_t)w0) : s.T;
   const bool there = slot > 0 && slot < c.num_slots;
   const int ring = c.ring_start[there ? slot : 0];
   e.p = pn;
   e.r = ring;
   e.mode = 2;
   int bit = 0;
-  if (e.T < 0 || e.T > s.T || e.bos < 0) {
+  if (e.bos < 0 || (s.cu && w1 < w0) || e.T > s.T) {  // (with w0 >= 0 and w1 >= w0 the difference cannot wrap)
     e.mode = 0;
     bit = SSU_STATUS_BAD_SEQLEN;
   } else if (!there) {

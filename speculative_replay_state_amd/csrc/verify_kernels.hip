@@ -65,8 +65,9 @@ __device__ __forceinline__ Verdict verdict(const KVerify &v, int b, int lane) {
   o.draft = -1;
   o.n = 0;
   o.bos = v.cu ? v.cu[b] : b * v.T;
-  o.T = v.cu ? v.cu[b + 1] - o.bos : v.T;
-  if (o.T < 0 || o.T > v.T || o.bos < 0) {
+  const int end = v.cu ? v.cu[b + 1] : o.bos + v.T;
+  o.T = (int)((uint32_t)end - (uint32_t)o.bos);
+  if (o.bos < 0 || end < o.bos || o.T > v.T) {  // (with 0 <= bos <= end the difference cannot wrap)
     o.bits = SSU_STATUS_BAD_SEQLEN;
     o.T = -1;
     return o;

@@ -199,6 +199,9 @@ def test_lengths_outside_the_limits():
     out, acc, status = run([1] * 8, p, None, [0.0] * 8, [0.5] * 3, 3, cu=[0, 4, 2, 5])
     assert status == ssu.SSU_STATUS_BAD_SEQLEN and acc.tolist() == [0, 0, 3]
     assert out.tolist() == [[-1] * 3, [-1] * 3, [1, 1, 1]]
+    # a length that is 1 only where the difference wraps
+    out, acc, status = run([1] * 8, p, None, [0.0] * 8, [0.5] * 2, 3, cu=[2 ** 31 - 1, -2 ** 31, 1])
+    assert status == ssu.SSU_STATUS_BAD_SEQLEN and acc.tolist() == [0, 0] and out.tolist() == [[-1] * 3] * 2
 
 
 def test_more_segments_than_threads():
