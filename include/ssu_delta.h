@@ -5,7 +5,8 @@
  *
  * Per value head h (key head h / (nheads_v / nheads_k)) with state
  * S [dim_v][dim_k], for every token t in order:
- *   g_t = A[h] dt',  dt' = softplus(dt_t[h] + dt_bias[h])   (or dt + dt_bias)
+ *   g_t = A[h] dt',  dt' = softplus(dt_t[h] + dt_bias[h])   (or dt + dt_bias),
+ *         at least -2^20 (exp is 0 from -104 on)
  *   b_t = sigmoid(beta_t[h])                                (or beta)
  *   k^ = k / sqrt(sum k^2 + 1e-6), q^ = q / sqrt(sum q^2 + 1e-6)  (or k, q)
  *   S <- exp(g_t) S;  u_t = b_t (v_t - S k^_t);  S <- S + u_t k^_t^T

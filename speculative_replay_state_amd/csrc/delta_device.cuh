@@ -146,10 +146,14 @@ __device__ __forceinline__ double scan_d(double v, int lane) {
   return v;
 }
 
+// g is kept at or above -2^20: its decay is 0 there as it is below, and the
+// differences of G around such a token keep their last bits (fp64 sums with
+// -1e12 in them resolve 1e-4, with -1e38 nothing, and with -inf they are NaN).
 __device__ __forceinline__ float2 delta_gate(float dt, float beta, float A, float bias, int softplus, int sigmoid) {
   const float d = dt + bias;
   float2 r;
   r.x = A * (softplus ? softplus_f(d) : d);
+  r.x = r.x < -0x1p20f ? -0x1p20f : r.x;  // (NaN stays)
   r.y = sigmoid ? 1.f / (1.f + expf(-beta)) : beta;
   return r;
 }

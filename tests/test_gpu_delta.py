@@ -459,6 +459,41 @@ def test_far_decays_do_not_overflow():
     R.check(h1[0].cpu(), S, went, R.tol(64, 32, 3, "f32"), "state")
 
 
+@pytest.mark.parametrize("big", [1e8, 1e30, float("inf")])
+def test_a_token_that_forgets_everything(big):
+    """One gate of -1e8 and less (past fp32's range too) among ordinary ones: the state before it is gone, the decays
+    between the tokens behind it are as exact as without it."""
+    g = gen(17)
+    x = R.inputs(g, 70, 1, 2, 64, 64)
+    x["A"] = torch.tensor([-1.0, -1e10])
+    x["dt"], x["dt_bias"] = 0.1 * torch.rand(70, 2, generator=g), torch.zeros(2)
+    x["dt"][:, 1] *= 1e-10
+    for t in (3, 40):
+        x["dt"][t] = big
+    gt = R.gates(x["dt"], x["beta"], x["A"], x["dt_bias"], softplus=False)
+    out = torch.empty(70, 2, 64, device=DEV)
+    h1 = torch.empty(1, 2, 64, 64, device=DEV)
+    call_prefill(up(x), [0, 70], out, None, h1, dt_softplus=False)
+    S, want = R.run(torch.zeros(2, 64, 64), x["q"], x["k"], x["v"], *gt, 0.125)
+    went = x["v"].double().transpose(0, 1).flatten(1).norm(dim=1)
+    R.check(out.cpu().transpose(0, 1), want.transpose(0, 1), 0.125 * went, R.tol(64, 32, 3, "f32"), "outputs")
+    R.check(h1[0].cpu(), S, went, R.tol(64, 32, 3, "f32"), "state")
+    # the same tokens through a ring of 16 after 5 of them, and folded
+    c = R.Cache(g, 2, 1, 2, 64, 64, 16, "f32")
+    d, dc = c.upload(ssu, DEV)
+    got = torch.empty(70, 2, 64, device=DEV)
+    call_step(dc, 10, [1], [4], None, up(x), got, dt_softplus=False)
+    k, v, gr, br = c.ring(1, 0, 4)
+    S0, _ = R.run(c.states(1), None, k, v, gr, br, 0.125)
+    S, want = R.run(S0, x["q"][:10], x["k"][:10], x["v"][:10], gt[0][:10], gt[1][:10], 0.125)
+    went = c.states(1).double().flatten(1).norm(dim=1) + torch.cat([v, x["v"][:10]]).double().transpose(0, 1).flatten(1).norm(dim=1)
+    R.check(got[:10].cpu().transpose(0, 1), want.transpose(0, 1), 0.125 * went, R.tol(64, 14, 1, "f32"), "step")
+    ssu.delta_flush(dc, i32([1]), i32([14]))
+    back = torch.empty(1, 2, 64, 64, device=DEV)
+    ssu.delta_read_state(dc, back, i32([1]))
+    R.check(back[0].cpu(), S, went, R.tol(64, 14, 1, "f32"), "folded")
+
+
 def test_repeated_keys():
     """The same key in every token with b near 1, where A is all ones below the
     diagonal and its powers would grow."""
