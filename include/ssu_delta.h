@@ -13,15 +13,20 @@
  *   o_t = scale S q^_t
  * Everything between the inputs and the outputs is computed in fp32 (decay
  * sums in fp64); matrix products take operands that are not bf16 in two or
- * three bf16 parts: fp32 states and outputs end within 1e-6 of their norm.  Infinities or NaN in a token's inputs may reach every
- * output of the call for its request and head (the tokens before it in the
- * call too), and nothing else.
+ * three bf16 parts: fp32 states and outputs end within 1e-6 of their norm.
+ * Infinities or NaN in a token's inputs may reach every output of the call for
+ * its request and head (the tokens before it in the call too), and nothing
+ * else.
  *
  * The conventions of ssu.h hold: device pointers owned by the caller, nothing
  * allocated or synchronised, every kernel on the given stream of the current
  * device (calls can be captured in a HIP graph), negative codes with
  * ssu_last_error() before any launch, contract violations that only the
- * device can see skipped with a bit in *status.
+ * device can see skipped with a bit in *status.  Sizes of buffers are the
+ * caller's: a slot id below num_slots names a page that exists, and the rows
+ * that a step's cu_seqlens names are rows of its tensors (a prefill checks
+ * them against `rows`).  Outputs must not overlap inputs except where it is
+ * said that they may.
  */
 #ifndef SSU_DELTA_H
 #define SSU_DELTA_H
@@ -52,8 +57,8 @@ extern "C" {
  * (ssu_delta_init_state and ssu_delta_read_state convert from and to plain
  * row-major fp32).
  * Requirements: dim_k 64 or 128, dim_v a multiple of 16 in [16, 256],
- * nheads_v % nheads_k == 0, nheads_v * dim_v < 2^23, 1 <= ring_len <= 32, state_dtype SSU_F32, SSU_BF16
- * or SSU_F16, io_dtype SSU_BF16; pointers 16-byte aligned (gate_cache 8-byte,
+ * nheads_v % nheads_k == 0, nheads_v * dim_v < 2^23, 1 <= ring_len <= 32,
+ * state_dtype SSU_F32, SSU_BF16 or SSU_F16, io_dtype SSU_BF16; pointers 16-byte aligned (gate_cache 8-byte,
  * ring_start and status 4-byte); strides at least one packed page and
  * multiples of 16 (gate_cache: of 8).  status may be NULL.
  */
@@ -84,8 +89,9 @@ typedef struct ssu_delta_cache {
  *   scale  the factor of q (dim_k^-1/2 in most layers)
  * Entry b's rows are b * max_seqlen + t, or [cu_seqlens[b], cu_seqlens[b+1]).
  * Requirements: 1 <= max_seqlen <= min(16, ring_len); q, k, v, out 16-byte
- * aligned, the rest 4-byte; batch * nheads_v <= SSU_DELTA_MAX_PAIRS.  Active slots
- * must be unique.  batch == 0 is a no-op.
+ * aligned, the rest 4-byte; batch * nheads_v <= SSU_DELTA_MAX_PAIRS.  Active
+ * slots must be unique, in a step as in a flush and an init.  batch == 0 is a
+ * no-op.
  */
 typedef struct ssu_delta_step {
   int32_t batch, max_seqlen;
@@ -147,11 +153,12 @@ int ssu_delta_read_state(const ssu_delta_cache *cache, float *states, int64_t st
  *         aligned; calls that may overlap need one each.
  * q, k, v, dt, beta, A, dt_bias, out and the flags as in ssu_delta_step.  A
  * sequence whose cu_seqlens are negative, decreasing or past rows is skipped
- * and ORs SSU_STATUS_BAD_SEQLEN into *status (when not NULL).
+ * and ORs SSU_STATUS_BAD_SEQLEN into *status (when not NULL); the results of
+ * the call's other sequences are then not to be relied on (nothing outside
+ * their rows and states is written).
  * Requirements: dim_k, dim_v and the heads as in ssu_delta_cache; rows *
  * nheads_v <= 2^30; num_seqs * nheads_v <= SSU_DELTA_MAX_PAIRS; row strides
- * below 2^23 elements.  num_seqs == 0
- * is a no-op; with rows == 0 the per-row tensors may be NULL.
+ * below 2^23 elements.  num_seqs == 0 is a no-op; with rows == 0 the per-row tensors may be NULL.
  */
 typedef struct ssu_delta_prefill_args {
   int32_t num_seqs, rows;

@@ -12,9 +12,10 @@
 // drafts' own (dependent) reads.  256 entries of 8 tokens, 131072 bf16 values in
 // two distributions: 27.9 us, 4.8 TB/s (32.1 in two launches); 64 entries,
 // 100003 fp32 values without draft probabilities (rows no 16 bytes apart):
-// 13.1 us; one entry of 32000: 8.7 us.  With four pieces a wave of verify_sum_kernel 36.7, 14.9 and
-// 10.5 us, with one 32.4, 13.1 and 8.9 (fewer waves wait for their drafts);
-// with the verdicts in a kernel of their own 31.6, 15.2, 11.9.
+// 13.1 us; one entry of 32000: 8.7 us.  With four pieces a wave of
+// verify_sum_kernel 36.7, 14.9 and 10.5 us, with one 32.4, 13.1 and 8.9 (fewer
+// waves wait for their drafts); with the verdicts in a kernel of their own
+// 31.6, 15.2, 11.9.
 #include "ssu_device.cuh"
 #include "verify_internal.h"
 

@@ -116,7 +116,10 @@ def inputs(gen, rows, hk, hv, dk, dv, wide=0):
 # the products may cancel, that of what went in (states and values).  Results
 # rounded to a type add half a step of it; operands towards bf16 outputs and
 # 16-bit checkpoints keep 16 bits, two parts on either side of a product: 3 x 2
-# x 2^-17.
+# x 2^-17.  (A prompt's and a flush's products with an fp32 state take it in two
+# parts as well, off by at most 2^-18 a value and at random: over the 64 and
+# more values of a row less than a fifth of 3 (dim_k + w) 2^-24, which counts
+# every addition of the sums at its worst.)
 def tol(dk, w, windows, dtype, state=None):
     """(part of the result's norm: its rounding, part of every norm)."""
     t = 3 * (dk + w) * 2.0 ** -24 * windows
