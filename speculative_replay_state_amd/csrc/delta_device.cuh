@@ -82,9 +82,15 @@ struct Tok<32> {
 };
 
 // x as a sum of NP bf16 values, each the nearest to what the ones before it
-// leave: relative error at most 2^-9, 2^-18, 2^-27 for 1, 2, 3 parts.
+// leave: relative error at most 2^-9, 2^-18, 2^-27 for 1, 2, 3 parts.  What a
+// pair leaves is a dot product with (-1, 0) and (0, -1) added to it, exact, one
+// instruction a value.  (-1 in the low half must come from a register: the
+// compiler, ROCm 7.2, writes it as the inline constant -1.0, which the
+// instruction takes as 0xBF800000, the other half.)
 template <int NP, int E, class V>
 __device__ __forceinline__ void split(const float (&x)[E], V (&out)[NP]) {
+  uint32_t low = 0xBF80u, high = 0xBF800000u;
+  asm("" : "+s"(low), "+s"(high));
   struct W { uint32_t w[E / 2]; };
   float rest[E];
 #pragma unroll
@@ -96,9 +102,9 @@ __device__ __forceinline__ void split(const float (&x)[E], V (&out)[NP]) {
     for (int i = 0; i < E / 2; ++i) {
       o.w[i] = pack_bf16(rest[2 * i], rest[2 * i + 1]);
       if (p + 1 < NP) {
-        asm("" : "+v"(o.w[i]));  // else the compiler converts the lower value a second time
-        rest[2 * i] -= bf2f(o.w[i] & 0xFFFFu);
-        rest[2 * i + 1] -= __uint_as_float(o.w[i] & 0xFFFF0000u);
+        const bf16x2 v = __builtin_bit_cast(bf16x2, o.w[i]);
+        rest[2 * i] = __builtin_amdgcn_fdot2_f32_bf16(v, __builtin_bit_cast(bf16x2, low), rest[2 * i], false);
+        rest[2 * i + 1] = __builtin_amdgcn_fdot2_f32_bf16(v, __builtin_bit_cast(bf16x2, high), rest[2 * i + 1], false);
       }
     }
     out[p] = __builtin_bit_cast(V, o);

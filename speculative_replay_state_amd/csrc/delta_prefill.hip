@@ -175,7 +175,9 @@ __global__ __launch_bounds__(64, 3) void delta_chunk_kernel(DPrefill p, int per,
 // 16-byte pieces of a chunk that NT threads stage, per thread.
 constexpr int pieces(int n, int NT) { return (n + NT - 1) / NT; }
 
-// What the waves of a chain share of a chunk.
+// What the waves of a chain share of a chunk.  (Rows that avoid the bank
+// conflicts of the transposed reads, 16 banks apart instead of 4, halve those
+// conflicts and change no time: 622 us either way for the 8 sequences below.)
 template <int DK, int COLS>
 struct Chunk {
   static constexpr int KS = DK + 8, VS = COLS + 8;  // row strides: 16 rows start in different banks
@@ -390,23 +392,57 @@ __device__ __forceinline__ void store_state(float *h1, int64_t at, bool on, cons
     for (int a = 0; a < 2; ++a) *reinterpret_cast<f32x4 *>(h1 + at + 32 * i + 4 * a) = S[i][a];
 }
 
+// The sequence at place `rank` by falling length (up to 64 of them and where
+// workgroups share a CU; else they are taken as they come), its rows in b0, b1;
+// false where the sequence is not what it has to be.
+__device__ __forceinline__ bool seq_of_rank(const DPrefill &p, int rank, int lane, int &seq, int &b0, int &b1) {
+  seq = rank;
+  if (p.n > 1 && p.n <= 64 && gridDim.x > 256) {
+    const int s = min(lane, p.n - 1);
+    const bool ok = seq_rows(p, s, b0, b1);
+    const int len = ok ? b1 - b0 : -1;
+    int before = lane < p.n ? 0 : 64;
+    for (int t = 0; t < p.n; ++t) {
+      const int other = __builtin_amdgcn_readlane(len, t);
+      before += other > len || (other == len && t < lane) ? 1 : 0;
+    }
+    seq = __builtin_ctzll(__ballot(before == rank));
+  }
+  return seq_rows(p, seq, b0, b1);
+}
+
 // Sequence, head and columns of a workgroup; false where the sequence is not
-// what it has to be (the first workgroup of its first head says so).  An XCD
-// takes neighbours, the column groups of a head and the heads of a key head,
-// which read the same chunks: with them spread over the XCDs 32 chains of
-// 16384 tokens took 687 us, as every L2 fetched them all.
+// what it has to be (the first workgroup of its first head says so).  Units of
+// workgroups, the column groups of a head or of the heads of a key head, read
+// the same chunks and share an XCD: with them spread over the XCDs 32 chains of
+// 16384 tokens took 687 us, as every L2 fetched them all.  The units go to the
+// XCDs in turn, longest sequences first, and of an XCD's 32 CUs the ones that
+// got the longest workgroups get the shortest ones beside them: 8 sequences of
+// 2048 to 4096 tokens, 64 heads, 696 us with a sequence to an XCD, 658 longest
+// first, 622 with the second 32 workgroups turned round.
 template <int COLS>
-__device__ __forceinline__ bool chain_of(const DPrefill &p, int groups, Chain &n, int &seq) {
-  const int tile = (int)xcd_tile(blockIdx.x, gridDim.x);
+__device__ __forceinline__ bool chain_of(const DPrefill &p, int groups, int unit, Chain &n, int &seq) {
+  const int last = min((int)(gridDim.x >> 3), 64) - 1;
+  int j = blockIdx.x >> 3;  // (XCD blockIdx.x & 7)
+  if (j >= 32 && j <= last) j = 32 + last - j;
+  const int tile = (j / unit * 8 + (blockIdx.x & 7)) * unit + j % unit;
   if (tile >= p.n * p.Hv * groups) return false;
   const int cg = tile % groups;
   n.h = tile / groups % p.Hv;
-  seq = tile / groups / p.Hv;
   n.c0 = cg * COLS;
-  const bool ok = seq_rows(p, seq, n.b0, n.b1);
+  const bool ok = seq_of_rank(p, tile / groups / p.Hv, threadIdx.x & 63, seq, n.b0, n.b1);
   if (!ok && p.status && cg == 0 && n.h == 0 && threadIdx.x == 0) atomicOr(p.status, SSU_STATUS_BAD_SEQLEN);
   n.chunks = (n.b1 - n.b0 + kChunk - 1) / kChunk;
   return ok;
+}
+// Workgroups of a unit: a key head's if that leaves every XCD about as many.
+inline int chain_unit(const DPrefill &p, int groups) {
+  const int64_t bundles = (int64_t)p.n * p.Hk;
+  return bundles % 8 == 0 || bundles >= 64 ? p.hpg * groups : groups;
+}
+inline dim3 chain_grid(const DPrefill &p, int groups, int unit) {
+  const int64_t units = (int64_t)p.n * p.Hv * groups / unit;
+  return dim3((unsigned)((units + 7) / 8 * 8 * unit));
 }
 
 // NC blocks of 16 columns of one chain, a wave each.  While chunk c is worked
@@ -416,13 +452,13 @@ __device__ __forceinline__ bool chain_of(const DPrefill &p, int groups, Chain &n
 // two workgroups share a CU (8 sequences of 2048 to 4096 tokens, 64 heads of
 // dim 128: 800 us with one and three buffers, 691 with two).
 template <int OT, int DK, int NC>
-__global__ __launch_bounds__(NC * 64, 2) void delta_scan_kernel(DPrefill p, int groups) {
+__global__ __launch_bounds__(NC * 64, 2) void delta_scan_kernel(DPrefill p, int groups, int unit) {
   constexpr int COLS = NC * 16, NK = DK / 32;
   __shared__ Chunk<DK, COLS> buf[2];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, m = lane & 15, q = lane >> 4;
   Chain n;
   int seq;
-  if (!chain_of<COLS>(p, groups, n, seq)) return;
+  if (!chain_of<COLS>(p, groups, unit, n, seq)) return;
   const int col = n.c0 + wave * 16;
   f32x4 S[NK][2];
   const int64_t state = (((int64_t)seq * p.Hv + n.h) * p.dv + col + m) * DK + 8 * q;
@@ -460,14 +496,14 @@ __global__ __launch_bounds__(NC * 64, 2) void delta_scan_kernel(DPrefill p, int 
 // those of chunks c - 1 and c the chain reads chunks c - 1 and c, the helpers
 // write chunk c + 1 and read c - 2: four buffers.
 template <int OT, int DK>
-__global__ __launch_bounds__((DK / 32 + 4) * 64, 1) void delta_chain_kernel(DPrefill p, int groups) {
+__global__ __launch_bounds__((DK / 32 + 4) * 64, 1) void delta_chain_kernel(DPrefill p, int groups, int unit) {
   constexpr int NS = DK / 32, NH = 4;
   __shared__ Chunk<DK, 16> buf[4];
   __shared__ f32x4 red_x[2][NS][2][64], red_o[3][NS][2][64], shared_u[2][2][64];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, m = lane & 15, q = lane >> 4;
   Chain n;
   int seq;
-  if (!chain_of<16>(p, groups, n, seq)) return;
+  if (!chain_of<16>(p, groups, unit, n, seq)) return;
   const uint8_t *rec0 = p.ws + ((int64_t)chunk_base(p, seq) * p.Hv + n.h) * kRecBytes;
   if (wave < NS) {
     f32x4 S[1][2];
@@ -541,23 +577,23 @@ __global__ __launch_bounds__((DK / 32 + 4) * 64, 1) void delta_chain_kernel(DPre
 
 template <int DK, int NC>
 hipError_t scan_launch(const DPrefill &p, int out_type, hipStream_t st) {
-  const int groups = (p.dv + NC * 16 - 1) / (NC * 16);
-  const dim3 grid(xcd_grid((int64_t)p.n * p.Hv * groups)), block(NC * 64);
+  const int groups = (p.dv + NC * 16 - 1) / (NC * 16), unit = chain_unit(p, groups);
+  const dim3 grid = chain_grid(p, groups, unit), block(NC * 64);
   if (out_type == kOutF32)
-    delta_scan_kernel<kOutF32, DK, NC><<<grid, block, 0, st>>>(p, groups);
+    delta_scan_kernel<kOutF32, DK, NC><<<grid, block, 0, st>>>(p, groups, unit);
   else
-    delta_scan_kernel<kOutBF16, DK, NC><<<grid, block, 0, st>>>(p, groups);
+    delta_scan_kernel<kOutBF16, DK, NC><<<grid, block, 0, st>>>(p, groups, unit);
   return hipGetLastError();
 }
 
 template <int DK>
 hipError_t chain_launch(const DPrefill &p, int out_type, hipStream_t st) {
-  const int groups = p.dv / 16;
-  const dim3 grid(xcd_grid((int64_t)p.n * p.Hv * groups)), block((DK / 32 + 4) * 64);
+  const int groups = p.dv / 16, unit = chain_unit(p, groups);
+  const dim3 grid = chain_grid(p, groups, unit), block((DK / 32 + 4) * 64);
   if (out_type == kOutF32)
-    delta_chain_kernel<kOutF32, DK><<<grid, block, 0, st>>>(p, groups);
+    delta_chain_kernel<kOutF32, DK><<<grid, block, 0, st>>>(p, groups, unit);
   else
-    delta_chain_kernel<kOutBF16, DK><<<grid, block, 0, st>>>(p, groups);
+    delta_chain_kernel<kOutBF16, DK><<<grid, block, 0, st>>>(p, groups, unit);
   return hipGetLastError();
 }
 
