@@ -16,11 +16,11 @@ constexpr float kDeltaEps = 1e-6f;     // under the root of the unit length of q
 constexpr int kDeltaMaxDv = 256;
 constexpr int kChunk = 32;             // tokens of a prompt chunk: one K = 32 MFMA step over tokens
 
-// Scratch of one (chunk, value head): T = (I + A)^-1 in fp32 and P in two
-// bf16 parts, as MFMA row operands without their zero upper blocks, then the
+// Scratch of one (chunk, value head): T - I, T = (I + A)^-1, and P in two bf16
+// parts, as MFMA row operands without their zero upper blocks, then the
 // chunk's factors.
-constexpr int kRecT = 3 * 64 * 16;     // blocks (0, 0), (1, 0), (1, 1): lane (m, q) row m, columns 4 q ..
-constexpr int kRecP = 2 * 64 * (8 + 16);  // rows 0..15: [part][lane] 8 bytes; rows 16..31: [part][lane] 16 bytes
+constexpr int kRecT = 2 * 64 * (8 + 16);  // rows 0..15: [part][lane] 8 bytes; rows 16..31: [part][lane] 16 bytes
+constexpr int kRecP = kRecT;
 constexpr int kRecF = 544;             // f32: b[32], b e^G rk[32], e^(Gw-G) rk[32], scale rq e^G[32], e^Gw
 constexpr int kRecBytes = kRecT + kRecP + kRecF;
 

@@ -7,17 +7,21 @@
 //   R = b (V - e^G K^ S^T),  U = T R,  O = scale e^G Q^ S^T + P U,
 //   S <- e^(G_w) S + (e^(G_w - G) U)^T K^,
 // by delta_scan_kernel (a wave per 16 columns of dim_v) where there are many
-// such chains, by delta_chain_kernel (eight waves per 16 columns) where there
+// such chains, by delta_chain_kernel (six waves per 16 columns) where there
 // are few and each chunk's latency adds up.  Products with q, k and v take them
 // as they are (bf16); the state enters the products with k and q in two bf16
-// parts, U the update in three and the outputs in two, T R is fp32.
+// parts, R the one with T - I in two (T - I too; the identity's share of U is
+// R in fp32), U the update in three and the outputs in two.  Against 64 bits,
+// fp32 states end 3e-7 to 8e-7 of their norm off, fp32 outputs 4e-6; with T R in
+// fp32 products the states 1e-7 to 2e-7, and the calls below 622 and 511 us.
 //
 // What bounds them, at 8 sequences of 2048 to 4096 tokens with 64 heads of dim
-// 128: the chunk kernel takes 140 us (0.4 GB of records written), the scan 550:
-// its matrix instructions are busy for half of that (a third of them the fp32
-// product with T) and the rest of its vector instructions for the other half,
-// which four waves a SIMD do not overlap.  One sequence of 16384 tokens, 32
-// heads: 50 us of chunks, then 0.95 us for each of 512.
+// 128, 593 us: the chunk kernel takes 140 us (0.4 GB of records written), the
+// scan 450; its matrix instructions are busy for two fifths of that and its
+// other vector instructions for as long, which four waves a SIMD hardly
+// overlap.  One sequence of 16384 tokens, 32 heads, 469 us: 56 us of chunks,
+// then 0.81 us for each of 512, a chain of 150 vector instructions, three
+// products and one exchange through LDS.
 #include <algorithm>
 
 #include "delta_device.cuh"
@@ -51,6 +55,27 @@ __device__ __forceinline__ bool seq_rows(const DPrefill &p, int s, int &b0, int 
   b1 = p.cu[s + 1];
   return b0 >= 0 && b0 <= b1 && b1 <= p.rows;
 }
+
+// Rows 16 ti .. of a 32 x 32 lower triangle as row operands of two bf16 parts,
+// [part][lane]; the first 16 rows are half as long.
+__device__ __forceinline__ void write_rows(uint8_t *at, int ti, int lane, const float (&x)[8]) {
+  bf16x8 f[2];
+  split<2>(x, f);
+#pragma unroll
+  for (int a = 0; a < 2; ++a) {
+    const u32x4 v = __builtin_bit_cast(u32x4, f[a]);
+    if (ti == 0)
+      st8(at + (a * 64 + lane) * 8, u32x2{v[0], v[1]});
+    else
+      st16(at + 2 * 64 * 8 + (a * 64 + lane) * 16, v);
+  }
+}
+// A row operand of them, part a; the first 16 rows' in the lower half.
+__device__ __forceinline__ u32x2 short_row(const uint8_t *at, int a, int lane) { return ld8(at + (a * 64 + lane) * 8); }
+__device__ __forceinline__ bf16x8 long_row(const uint8_t *at, int a, int lane) {
+  return __builtin_bit_cast(bf16x8, ld16(at + 2 * 64 * 8 + (a * 64 + lane) * 16));
+}
+__device__ __forceinline__ bf16x8 halves(u32x2 a, u32x2 b) { return __builtin_bit_cast(bf16x8, u32x4{a[0], a[1], b[0], b[1]}); }
 
 // A wave takes a chunk of one key head: k . k and k . q once, then T and P of
 // `per` of the value heads that share it.
@@ -138,16 +163,7 @@ __global__ __launch_bounds__(64, 3) void delta_chunk_kernel(DPrefill p, int per,
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           x[4 * a + e] = a <= ti && 16 * a + 4 * q + e <= i ? r * decay[a <= ti ? ti + a : 0][e] * qk[a <= ti ? ti + a : 0][e] : 0.f;
-      bf16x8 f[2];
-      split<2>(x, f);
-#pragma unroll
-      for (int a = 0; a < 2; ++a) {
-        const u32x4 v = __builtin_bit_cast(u32x4, f[a]);
-        if (ti == 0)
-          st8(rec + kRecT + (a * 64 + lane) * 8, u32x2{v[0], v[1]});
-        else
-          st16(rec + kRecT + 2 * 64 * 8 + (a * 64 + lane) * 16, v);
-      }
+      write_rows(rec + kRecT, ti, lane, x);
     }
     wave_sync();
     invert_diag<kChunk>(w, lane);
@@ -156,8 +172,8 @@ __global__ __launch_bounds__(64, 3) void delta_chunk_kernel(DPrefill p, int per,
       float x[8];
       t_row<kChunk>(w, ti, m, q, x);
 #pragma unroll
-      for (int a = 0; a <= ti; ++a)
-        st16(rec + ((ti + a) * 64 + lane) * 16, __builtin_bit_cast(u32x4, f32x4{x[4 * a], x[4 * a + 1], x[4 * a + 2], x[4 * a + 3]}));
+      for (int e = 0; e < 4; ++e) x[4 * ti + e] = 4 * q + e == m ? 0.f : x[4 * ti + e];  // T - I
+      write_rows(rec, ti, lane, x);
     }
     float *f = reinterpret_cast<float *>(rec + kRecT + kRecP);
     if (lane < kChunk) {
@@ -249,86 +265,81 @@ struct Stage {
 // the state the rows n = n0 + 32 i + 8 q + 4 a + r in S[i][a][r], of the tokens
 // the rows 16 ti + 4 q + r.
 
-// x += K S^T (rows = tokens), o += Q S^T (transposed: columns = tokens), over
-// the wave's rows of the state; S in 16 of its 24 bits, which moves a state by
-// 2^-20.6 of its norm in the mean (two bf16 parts, each rounded to nearest).
-template <int DK, int COLS, int NK>
-__device__ __forceinline__ void state_products(const Chunk<DK, COLS> &in, const f32x4 (&S)[NK][2], int n0, int m, int q,
-                                               f32x4 (&x)[2], f32x4 (&o)[2]) {
-#pragma unroll
-  for (int i = 0; i < NK; ++i) {
-    bf16x8 fs[2], kf[2], qf[2];
-    float y[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) y[e] = S[i][e / 4][e % 4];
-    split<2>(y, fs);
-#pragma unroll
-    for (int ti = 0; ti < 2; ++ti) {
-      const int at = (16 * ti + m) * in.KS + n0 + 32 * i + 8 * q;
-      kf[ti] = __builtin_bit_cast(bf16x8, ld16(in.k + at));
-      qf[ti] = __builtin_bit_cast(bf16x8, ld16(in.q + at));
-    }
-#pragma unroll
-    for (int a = 1; a >= 0; --a)
-#pragma unroll
-      for (int ti = 0; ti < 2; ++ti) {
-        x[ti] = mfma_bf16(kf[ti], fs[a], x[ti]);
-        o[ti] = mfma_bf16(fs[a], qf[ti], o[ti]);
-      }
-  }
+// S in 16 of its 24 bits enters the products with k and q, which moves a state
+// by 2^-20.6 of its norm in the mean (two bf16 parts, each rounded to nearest).
+__device__ __forceinline__ void split_state(const f32x4 (&S)[2], bf16x8 (&f)[2]) {
+  const float y[8] = {S[0][0], S[0][1], S[0][2], S[0][3], S[1][0], S[1][1], S[1][2], S[1][3]};
+  split<2>(y, f);
+}
+// 16 tokens of k or q along n0 .. n0 + 31
+template <int DK>
+__device__ __forceinline__ bf16x8 row_tile(const uint16_t *rows, int n0, int ti, int lane) {
+  return __builtin_bit_cast(bf16x8, ld16(rows + (16 * ti + (lane & 15)) * (DK + 8) + n0 + 8 * (lane >> 4)));
 }
 
-// U = T (b V - (b e^G / |k|) K S^T), T and the product in fp32.
+// What a chunk's residuals and update take from LDS beside k.
 template <int DK, int COLS>
-__device__ __forceinline__ void residuals(const Chunk<DK, COLS> &in, int block, int lane, const f32x4 (&x)[2], f32x4 (&U)[2]) {
-  const int m = lane & 15, q = lane >> 4;
-  const float *fac = in.factors();
-  const f32x4 *T = reinterpret_cast<const f32x4 *>(in.rec) + lane;
-  const f32x4 t00 = T[0], t10 = T[64], t11 = T[128];
-  f32x4 R[2];
-#pragma unroll
-  for (int ti = 0; ti < 2; ++ti) {
-    const f32x4 b = *reinterpret_cast<const f32x4 *>(fac + 16 * ti + 4 * q);
-    const f32x4 be = *reinterpret_cast<const f32x4 *>(fac + 32 + 16 * ti + 4 * q);
-    const s16x4 v = lds_tr4(in.v + (16 * ti + 4 * q + (m >> 2)) * in.VS + block * 16 + 4 * (m & 3));
-#pragma unroll
-    for (int r = 0; r < 4; ++r) R[ti][r] = fmaf(-be[r], x[ti][r], b[r] * bf2f((uint16_t)v[r]));
-    U[ti] = f32x4{0.f, 0.f, 0.f, 0.f};
-  }
-  f32x4 u = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    U[0] = mfma_f32(t00[i], R[0][i], U[0]);
-    U[1] = mfma_f32(t10[i], R[0][i], U[1]);
-    u = mfma_f32(t11[i], R[1][i], u);
-  }
-  U[1] += u;
-}
-
-// S <- e^(G_w) S + (e^(G_w - G) U / |k|)^T K, the product from 24 bits of U.
-template <int DK, int COLS, int NK>
-__device__ __forceinline__ void update_state(const Chunk<DK, COLS> &in, f32x4 (&S)[NK][2], int n0, int lane, const f32x4 (&U)[2]) {
-  const int m = lane & 15, q = lane >> 4;
-  const float *fac = in.factors();
-  float y[8];
-#pragma unroll
-  for (int ti = 0; ti < 2; ++ti) {
-    const f32x4 e = *reinterpret_cast<const f32x4 *>(fac + 64 + 16 * ti + 4 * q);
-#pragma unroll
-    for (int r = 0; r < 4; ++r) y[4 * ti + r] = U[ti][r] * e[r];
-  }
-  bf16x8 f[3];
-  split<3>(y, f);
-  const float ew = fac[128];
-#pragma unroll
-  for (int i = 0; i < NK; ++i)
+struct Factors {
+  u32x2 ts[2];  // T's rows in two parts
+  bf16x8 tl[2];
+  f32x4 b[2], be[2], e[2];  // b, b e^G / |k|, e^(G_w - G) / |k| of the lane's tokens
+  s16x4 v[2];
+  float ew;
+  __device__ __forceinline__ void load_residual(const Chunk<DK, COLS> &in, int block, int lane) {
+    const int m = lane & 15, q = lane >> 4;
+    const float *fac = in.factors();
 #pragma unroll
     for (int a = 0; a < 2; ++a) {
-      // row m = 4 j + r of the tile is n = 32 i + 8 j + 4 a + r
-      const uint16_t *at = in.k + (4 * q + (m >> 2)) * in.KS + n0 + 32 * i + 8 * (m & 3) + 4 * a;
-      struct { s16x4 lo, hi; } kt = {lds_tr4(at), lds_tr4(at + 16 * in.KS)};
-      S[i][a] = Tok<32>::exact<true>(__builtin_bit_cast(bf16x8, kt), f, scale4(S[i][a], ew));
+      ts[a] = short_row(in.rec, a, lane);
+      tl[a] = long_row(in.rec, a, lane);
     }
+#pragma unroll
+    for (int ti = 0; ti < 2; ++ti) {
+      b[ti] = *reinterpret_cast<const f32x4 *>(fac + 16 * ti + 4 * q);
+      be[ti] = *reinterpret_cast<const f32x4 *>(fac + 32 + 16 * ti + 4 * q);
+      v[ti] = lds_tr4(in.v + (16 * ti + 4 * q + (m >> 2)) * in.VS + block * 16 + 4 * (m & 3));
+    }
+  }
+  __device__ __forceinline__ void load_update(const Chunk<DK, COLS> &in, int lane) {
+    const float *fac = in.factors();
+#pragma unroll
+    for (int ti = 0; ti < 2; ++ti) e[ti] = *reinterpret_cast<const f32x4 *>(fac + 64 + 16 * ti + 4 * (lane >> 4));
+    ew = fac[128];
+  }
+  // U = R + (T - I) R with R = b V - (b e^G / |k|) K S^T: the identity's part in
+  // fp32, the other from T - I and R in two parts each.  (The first 16 tokens have
+  // only themselves before them: two products of parts fill a depth of 32.)
+  __device__ __forceinline__ void residuals(const f32x4 (&x)[2], f32x4 (&U)[2]) const {
+    float R[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      R[i] = fmaf(-be[i / 4][i % 4], x[i / 4][i % 4], b[i / 4][i % 4] * bf2f((uint16_t)v[i / 4][i % 4]));
+    bf16x8 f[2];
+    split<2>(R, f);
+    const u32x4 r0 = __builtin_bit_cast(u32x4, f[0]), r1 = __builtin_bit_cast(u32x4, f[1]);
+    const bf16x8 ts01 = halves(ts[0], ts[1]);
+    U[0] = mfma_bf16(ts01, halves(u32x2{r1[0], r1[1]}, u32x2{r1[0], r1[1]}), f32x4{R[0], R[1], R[2], R[3]});
+    U[1] = mfma_bf16(tl[1], f[0], f32x4{R[4], R[5], R[6], R[7]});
+    U[0] = mfma_bf16(ts01, halves(u32x2{r0[0], r0[1]}, u32x2{r0[0], r0[1]}), U[0]);
+    U[1] = mfma_bf16(tl[0], f[1], U[1]);
+    U[1] = mfma_bf16(tl[0], f[0], U[1]);
+  }
+  // e^(G_w - G) U / |k| in 24 bits
+  __device__ __forceinline__ void update(const f32x4 (&U)[2], bf16x8 (&f)[3]) const {
+    float y[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = U[i / 4][i % 4] * e[i / 4][i % 4];
+    split<3>(y, f);
+  }
+};
+
+// k transposed: tokens along the depth; row m = 4 j + r of the tile is n = n0 + 8 j + 4 a + r
+template <int DK, int COLS>
+__device__ __forceinline__ bf16x8 key_tile(const Chunk<DK, COLS> &in, int n0, int a, int lane) {
+  const int m = lane & 15, q = lane >> 4;
+  const uint16_t *at = in.k + (4 * q + (m >> 2)) * in.KS + n0 + 8 * (m & 3) + 4 * a;
+  struct { s16x4 lo, hi; } kt = {lds_tr4(at), lds_tr4(at + 16 * in.KS)};
+  return __builtin_bit_cast(bf16x8, kt);
 }
 
 // Outputs of tokens 16 ti .. of a chunk: (scale e^G / |q|) Q S^T + P U, from o =
@@ -345,17 +356,7 @@ __device__ __forceinline__ void write_outputs(const DPrefill &p, const Chain &n,
                                                       rows * row_bytes, 0x00020000);
   bf16x8 f[2];
 #pragma unroll
-  for (int a = 0; a < 2; ++a) {
-    u32x4 v = {0, 0, 0, 0};
-    if (ti == 0) {
-      const u32x2 lo = ld8(in.rec + kRecT + (a * 64 + lane) * 8);
-      v[0] = lo[0];
-      v[1] = lo[1];
-    } else {
-      v = ld16(in.rec + kRecT + 2 * 64 * 8 + (a * 64 + lane) * 16);
-    }
-    f[a] = __builtin_bit_cast(bf16x8, v);
-  }
+  for (int a = 0; a < 2; ++a) f[a] = ti == 0 ? halves(short_row(in.rec + kRecT, a, lane), u32x2{0, 0}) : long_row(in.rec + kRecT, a, lane);
   const int t = 16 * ti + m;
   o = mfma_parts(fu, f, scale4(o, in.factors()[96 + t]));
   const int at = t < rows && col < p.dv && on ? t * row_bytes + (n.h * p.dv + col + 4 * q) * kOut : 0x7FFFFFF0;
@@ -418,7 +419,7 @@ __device__ __forceinline__ bool seq_of_rank(const DPrefill &p, int rank, int lan
 // 16384 tokens took 687 us, as every L2 fetched them all.  The units go to the
 // XCDs in turn, longest sequences first, and of an XCD's 32 CUs the ones that
 // got the longest workgroups get the shortest ones beside them: 8 sequences of
-// 2048 to 4096 tokens, 64 heads, 696 us with a sequence to an XCD, 658 longest
+// 2048 to 4096 tokens, 64 heads, 696 us (with T R in fp32 products) with a sequence to an XCD, 658 longest
 // first, 622 with the second 32 workgroups turned round.
 template <int COLS>
 __device__ __forceinline__ bool chain_of(const DPrefill &p, int groups, int unit, Chain &n, int &seq) {
@@ -476,10 +477,36 @@ __global__ __launch_bounds__(NC * 64, 2) void delta_scan_kernel(DPrefill p, int 
       st.fetch(p, n, rec0, c + 2, tid);
       f32x4 x[2], o[2], U[2];
       x[0] = x[1] = o[0] = o[1] = f32x4{0.f, 0.f, 0.f, 0.f};
-      state_products(in, S, 0, m, q, x, o);
-      residuals(in, wave, lane, x, U);
-      update_state(in, S, 0, lane, U);
-      bf16x8 fu[2];
+      // x = K S^T (rows = tokens), o = Q S^T (transposed: columns = tokens)
+#pragma unroll
+      for (int i = 0; i < NK; ++i) {
+        bf16x8 fs[2], kf[2], qf[2];
+        split_state(S[i], fs);
+#pragma unroll
+        for (int ti = 0; ti < 2; ++ti) {
+          kf[ti] = row_tile<DK>(in.k, 32 * i, ti, lane);
+          qf[ti] = row_tile<DK>(in.q, 32 * i, ti, lane);
+        }
+#pragma unroll
+        for (int a = 1; a >= 0; --a)
+#pragma unroll
+          for (int ti = 0; ti < 2; ++ti) {
+            x[ti] = mfma_bf16(kf[ti], fs[a], x[ti]);
+            o[ti] = mfma_bf16(fs[a], qf[ti], o[ti]);
+          }
+      }
+      Factors<DK, COLS> fac;
+      fac.load_residual(in, wave, lane);
+      fac.residuals(x, U);
+      // S <- e^(G_w) S + (e^(G_w - G) U / |k|)^T K
+      fac.load_update(in, lane);
+      bf16x8 fw[3], fu[2];
+      fac.update(U, fw);
+#pragma unroll
+      for (int i = 0; i < NK; ++i)
+#pragma unroll
+        for (int a = 0; a < 2; ++a)
+          S[i][a] = Tok<32>::exact<true>(key_tile(in, 32 * i, a, lane), fw, scale4(S[i][a], fac.ew));
       split_u(U, fu);
 #pragma unroll
       for (int ti = 0; ti < 2; ++ti) write_outputs<OT>(p, n, in, c, ti, col, true, lane, fu, o[ti]);
@@ -492,49 +519,93 @@ __global__ __launch_bounds__(NC * 64, 2) void delta_scan_kernel(DPrefill p, int 
 // is all that counts: DK / 32 waves hold 32 rows n of the state each and sum
 // their products with k through LDS; four more waves keep everything else off
 // the chain, the chunks' way into LDS and the outputs, which they form two
-// chunks behind.  One barrier a chunk (where the sums are exchanged); between
-// those of chunks c - 1 and c the chain reads chunks c - 1 and c, the helpers
-// write chunk c + 1 and read c - 2: four buffers.
+// chunks behind.  One barrier a chunk (where the sums are exchanged).  Behind
+// that of chunk c the chain reads what chunk c + 1 needs into registers and
+// forms its part of Q S^T while the sums are on their way, so that only they,
+// the residuals and the update lie between two barriers' products.  The
+// helpers write chunk c + 2 and read c - 1 meanwhile: four buffers.
 template <int OT, int DK>
-__global__ __launch_bounds__((DK / 32 + 4) * 64, 1) void delta_chain_kernel(DPrefill p, int groups, int unit) {
-  constexpr int NS = DK / 32, NH = 4;
-  __shared__ Chunk<DK, 16> buf[4];
-  __shared__ f32x4 red_x[2][NS][2][64], red_o[3][NS][2][64], shared_u[2][2][64];
+__global__ __launch_bounds__(6 * 64, 1) void delta_chain_kernel(DPrefill p, int groups, int unit) {
+  constexpr int NS = 2, NH = 4, NK = DK / 32 / NS;
+  typedef Chunk<DK, 16> Buf;
+  __shared__ Buf buf[4];
+  __shared__ f32x4 red_x[2][NS][2][64], red_o[2][NS][2][64], shared_u[2][2][64];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, m = lane & 15, q = lane >> 4;
   Chain n;
   int seq;
   if (!chain_of<16>(p, groups, unit, n, seq)) return;
   const uint8_t *rec0 = p.ws + ((int64_t)chunk_base(p, seq) * p.Hv + n.h) * kRecBytes;
   if (wave < NS) {
-    f32x4 S[1][2];
-    const int64_t state = (((int64_t)seq * p.Hv + n.h) * p.dv + n.c0 + m) * DK + wave * 32 + 8 * q;
+    const int n0 = wave * NK * 32;
+    f32x4 S[NK][2];
+    const int64_t state = (((int64_t)seq * p.Hv + n.h) * p.dv + n.c0 + m) * DK + n0 + 8 * q;
     load_state(p.h0, state, true, S);
     if (n.chunks > 0) {
       __builtin_amdgcn_s_setprio(2);
       __syncthreads();
-      for (int c = 0; c < n.chunks; ++c) {
-        const Chunk<DK, 16> &in = buf[c & 3];
-        f32x4 x[2], o[2], U[2];
-        x[0] = x[1] = o[0] = o[1] = f32x4{0.f, 0.f, 0.f, 0.f};
-        state_products(in, S, wave * 32, m, q, x, o);
+      struct Held {
+        bf16x8 k[NK][2], q[NK][2], kt[NK][2];
+        Factors<DK, 16> fac;
+      };
+      auto hold = [&](int c, Held &h) {
+        const Buf &in = buf[c & 3];
 #pragma unroll
-        for (int ti = 0; ti < 2; ++ti) {
-          red_x[c & 1][wave][ti][lane] = x[ti];
-          red_o[c % 3][wave][ti][lane] = o[ti];
-        }
+        for (int i = 0; i < NK; ++i)
+#pragma unroll
+          for (int ti = 0; ti < 2; ++ti) {
+            h.k[i][ti] = row_tile<DK>(in.k, n0 + 32 * i, ti, lane);
+            h.q[i][ti] = row_tile<DK>(in.q, n0 + 32 * i, ti, lane);
+            h.kt[i][ti] = key_tile(in, n0 + 32 * i, ti, lane);
+          }
+        h.fac.load_residual(in, 0, lane);
+        h.fac.load_update(in, lane);
+      };
+      auto step = [&](int c, const Held &has, Held &next) {
+        bf16x8 fs[NK][2];
+        f32x4 x[2], o[2], U[2], other[2];
+        x[0] = x[1] = o[0] = o[1] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < NK; ++i) split_state(S[i], fs[i]);
+#pragma unroll
+        for (int i = 0; i < NK; ++i)
+#pragma unroll
+          for (int a = 1; a >= 0; --a)
+#pragma unroll
+            for (int ti = 0; ti < 2; ++ti) x[ti] = mfma_bf16(has.k[i][ti], fs[i][a], x[ti]);
+#pragma unroll
+        for (int ti = 0; ti < 2; ++ti) red_x[c & 1][wave][ti][lane] = x[ti];
         __syncthreads();
 #pragma unroll
-        for (int ti = 0; ti < 2; ++ti) {
-          x[ti] = red_x[c & 1][0][ti][lane];
+        for (int ti = 0; ti < 2; ++ti) other[ti] = red_x[c & 1][1 - wave][ti][lane];
+        __builtin_amdgcn_sched_barrier(0);  // (LDS answers in order: these first)
+        hold(c + 1, next);  // (behind the last chunk: its last buffer's neighbour, not used)
 #pragma unroll
-          for (int w = 1; w < NS; ++w) x[ti] += red_x[c & 1][w][ti][lane];
+        for (int i = 0; i < NK; ++i)
+#pragma unroll
+          for (int a = 1; a >= 0; --a)
+#pragma unroll
+            for (int ti = 0; ti < 2; ++ti) o[ti] = mfma_bf16(fs[i][a], has.q[i][ti], o[ti]);
+#pragma unroll
+        for (int ti = 0; ti < 2; ++ti) x[ti] += other[ti];
+        has.fac.residuals(x, U);
+        bf16x8 fw[3];
+        has.fac.update(U, fw);
+#pragma unroll
+        for (int i = 0; i < NK; ++i)
+#pragma unroll
+          for (int a = 0; a < 2; ++a) S[i][a] = Tok<32>::exact<true>(has.kt[i][a], fw, scale4(S[i][a], has.fac.ew));
+#pragma unroll
+        for (int ti = 0; ti < 2; ++ti) {
+          red_o[c & 1][wave][ti][lane] = o[ti];
+          if (wave == 0) shared_u[c & 1][ti][lane] = U[ti];
         }
-        residuals(in, 0, lane, x, U);
-        if (wave == 0) {
-          shared_u[c & 1][0][lane] = U[0];
-          shared_u[c & 1][1][lane] = U[1];
-        }
-        update_state(in, S, wave * 32, lane, U);
+      };
+      Held one, two;
+      hold(0, one);
+      for (int c = 0; c < n.chunks; c += 2) {
+        step(c, one, two);
+        if (c + 1 >= n.chunks) break;
+        step(c + 1, two, one);
       }
       __syncthreads();
     }
@@ -543,31 +614,31 @@ __global__ __launch_bounds__((DK / 32 + 4) * 64, 1) void delta_chain_kernel(DPre
     const int ht = tid - NS * 64, hw = wave - NS;
     // outputs of tokens 16 (hw % 2) .. of chunk c, by helpers 0 and 1
     auto outputs = [&](int c) {
-      f32x4 o = red_o[c % 3][0][hw & 1][lane];
+      f32x4 o = red_o[c & 1][0][hw & 1][lane];
 #pragma unroll
-      for (int w = 1; w < NS; ++w) o += red_o[c % 3][w][hw & 1][lane];
+      for (int w = 1; w < NS; ++w) o += red_o[c & 1][w][hw & 1][lane];
       const f32x4 U[2] = {shared_u[c & 1][0][lane], shared_u[c & 1][1][lane]};
       bf16x8 fu[2];
       split_u(U, fu);
       write_outputs<OT>(p, n, buf[c & 3], c, hw & 1, n.c0, hw < 2, lane, fu, o);
     };
-    // chunk c + 2 is fetched while c + 1 is stored: two register sets, so that
-    // a chunk has more than an iteration to arrive
-    Stage<DK, 16, NH * 64> st[2];
-    st[0].fetch(p, n, rec0, 0, ht);
-    st[1].fetch(p, n, rec0, 1, ht);
+    // chunk c + SETS is fetched while c + 1 is stored: as many register sets, so
+    // that a chunk has several iterations to arrive
+    constexpr int SETS = 4;
+    Stage<DK, 16, NH * 64> st[SETS];
+#pragma unroll
+    for (int i = 0; i < SETS; ++i) st[i].fetch(p, n, rec0, i, ht);
     st[0].store(buf[0], ht);
     __syncthreads();
-    auto serve = [&](int c, Stage<DK, 16, NH * 64> &has, Stage<DK, 16, NH * 64> &free) {
-      free.fetch(p, n, rec0, c + 2, ht);
-      has.store(buf[(c + 1) & 3], ht);
-      if (c >= 2) outputs(c - 2);
-      __syncthreads();
-    };
-    for (int c = 0; c < n.chunks; c += 2) {
-      serve(c, st[1], st[0]);
-      if (c + 1 >= n.chunks) break;
-      serve(c + 1, st[0], st[1]);
+    for (int c = 0; c < n.chunks; c += SETS) {
+#pragma unroll
+      for (int i = 0; i < SETS; ++i) {
+        if (c + i >= n.chunks) break;
+        st[i].fetch(p, n, rec0, c + i + SETS, ht);
+        st[(i + 1) % SETS].store(buf[(c + i + 1) & 3], ht);
+        if (c + i >= 2) outputs(c + i - 2);
+        __syncthreads();
+      }
     }
     if (n.chunks >= 2) outputs(n.chunks - 2);
     __syncthreads();
@@ -589,7 +660,7 @@ hipError_t scan_launch(const DPrefill &p, int out_type, hipStream_t st) {
 template <int DK>
 hipError_t chain_launch(const DPrefill &p, int out_type, hipStream_t st) {
   const int groups = p.dv / 16, unit = chain_unit(p, groups);
-  const dim3 grid = chain_grid(p, groups, unit), block((DK / 32 + 4) * 64);
+  const dim3 grid = chain_grid(p, groups, unit), block(6 * 64);
   if (out_type == kOutF32)
     delta_chain_kernel<kOutF32, DK><<<grid, block, 0, st>>>(p, groups, unit);
   else
