@@ -40,7 +40,7 @@ extern "C" {
 
 /* (entry, value head) pairs one call may cover: every launch grid, in
  * threads, then fits 32 bits.  Calls past it return SSU_ERR_UNSUPPORTED. */
-#define SSU_DELTA_MAX_PAIRS ((1 << 22) - 1)
+#define SSU_DELTA_MAX_PAIRS (1 << 21)
 
 /*
  * The per-slot cache.  Inside a slot page every tensor is packed; the

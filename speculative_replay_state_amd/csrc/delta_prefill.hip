@@ -682,13 +682,14 @@ hipError_t prefill_dk(const DPrefill &p, int out_type, hipStream_t st) {
   const hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;
   // Few chains: a workgroup to a block of 16 columns while each gets a CU of its
-  // own (2048 tokens, dim 128, us of chain, half-head, whole-head workgroups:
-  // 32 chains 89, 134, 181; 64 chains 162, 139, 185).  Many: a workgroup holds a
-  // whole head, two of them a CU (256 chains 554, 233, 213; 512 chains 917, 404,
-  // 338; 128 chains 302, 150, 193); up to 64 columns are four waves either way.
+  // own.  Many: a workgroup holds a whole head, two of them a CU; up to 64
+  // columns are four waves either way.  Sequences of up to 2048 tokens, dim 128,
+  // us of chain, half-head, whole-head workgroups: 32 chains 77, 120, 164; 64
+  // chains 135, 125, 169; 256 chains 399, 193, 200; 512 chains 772, 358, 333.
+  // Dim 64, 700 tokens: 64 chains 29, 39; 128 chains 44, 42.
   const int64_t chains = (int64_t)p.n * p.Hv;
   if (chains * (p.dv / 16) <= 256) return chain_launch<DK>(p, out_type, st);
-  if (p.dv > 64 && chains >= 256) return scan_launch<DK, 8>(p, out_type, st);
+  if (p.dv > 64 && chains > 256) return scan_launch<DK, 8>(p, out_type, st);
   return scan_launch<DK, 4>(p, out_type, st);
 }
 

@@ -12,7 +12,7 @@ import dataclasses
 
 from . import (DTYPE_CODES, SSU_BF16, SSU_F32, _check, _lib, _on_device, _packed, _ptr, _slot_pages, _I32, _I64, _P)
 
-SSU_DELTA_MAX_PAIRS = (1 << 22) - 1
+SSU_DELTA_MAX_PAIRS = 1 << 21
 
 
 class SsuDeltaCache(ctypes.Structure):

@@ -371,7 +371,7 @@ def test_prefill(lens, hk, hv, dk, dv, init, out_name):
 
 
 # the chains (sequence, value head) that each scan kernel takes: up to 256 blocks of 16 columns one kernel, more another,
-# from 256 chains of more than 64 columns a third
+# over 256 chains of more than 64 columns a third
 @pytest.mark.parametrize("n,most,hk,hv,dk,dv,init", [(9, 70, 2, 4, 128, 128, True), (20, 90, 4, 8, 64, 64, True),
                                                      (20, 100, 2, 8, 128, 48, False), (40, 100, 4, 8, 128, 128, True),
                                                      (33, 66, 2, 8, 64, 144, False), (64, 40, 1, 4, 64, 256, True)])
@@ -425,20 +425,20 @@ def test_prefill_bad_sequences_are_skipped_and_named():
             assert bool((h1[s] == 7).all()) == (s not in good)
 
 
-@pytest.mark.parametrize("n", [150])
-def test_many_short_sequences_find_their_chunks(n):
+@pytest.mark.parametrize("n,dv", [(150, 16), (150, 80)])
+def test_many_short_sequences_find_their_chunks(n, dv):
     """More sequences than lanes look at once, empty ones among them."""
     g = gen(13)
     lens = torch.randint(0, 40, (n,), generator=g)
     lens[::7] = 0
     cu = [0] + lens.cumsum(0).tolist()
-    x = R.inputs(g, cu[-1], 1, 1, 64, 16)
-    out = torch.empty(cu[-1], 1, 16, device=DEV)
+    x = R.inputs(g, cu[-1], 1, 1, 64, dv)
+    out = torch.empty(cu[-1], 1, dv, device=DEV)
     call_prefill(up(x), cu, out)
     gt = R.gates(x["dt"], x["beta"], x["A"], x["dt_bias"])
     for s in range(n):
         at = slice(cu[s], cu[s + 1])
-        _, want = R.run(torch.zeros(1, 16, 64), x["q"][at], x["k"][at], x["v"][at], gt[0][at], gt[1][at], 0.125)
+        _, want = R.run(torch.zeros(1, dv, 64), x["q"][at], x["k"][at], x["v"][at], gt[0][at], gt[1][at], 0.125)
         R.check(out[at].cpu().transpose(0, 1), want.transpose(0, 1), 0.125 * float(x["v"][at].double().norm()),
                 R.tol(64, 32, 2, "f32"), "sequence %d" % s)
 
