@@ -16,11 +16,11 @@
 // fp32 products the states 1e-7 to 2e-7, and the calls below 622 and 511 us.
 //
 // What bounds them, at 8 sequences of 2048 to 4096 tokens with 64 heads of dim
-// 128, 593 us: the chunk kernel takes 140 us (0.4 GB of records written), the
-// scan 450; its matrix instructions are busy for two fifths of that and its
+// 128, 600 us: the chunk kernel takes 118 us (0.32 GB of records written), the
+// scan 480; its matrix instructions are busy for two fifths of that and its
 // other vector instructions for as long, which four waves a SIMD hardly
-// overlap.  One sequence of 16384 tokens, 32 heads, 469 us: 56 us of chunks,
-// then 0.81 us for each of 512, a chain of 150 vector instructions, three
+// overlap.  One sequence of 16384 tokens, 32 heads, 468 us: 50 us of chunks,
+// then 0.82 us for each of 512, a chain of 150 vector instructions, three
 // products and one exchange through LDS.
 #include <algorithm>
 
@@ -672,9 +672,9 @@ template <int DK>
 hipError_t prefill_dk(const DPrefill &p, int out_type, hipStream_t st) {
   const int64_t chunks = (int64_t)p.rows / kChunk + p.n;
   // Value heads of a chunk in one wave, which forms its k . k and k . q for all
-  // of them once: as many as leave 4 waves a SIMD.  8 value heads a key head,
-  // 2048 tokens: 170 us of 32 heads with 1 in a wave, 184 with 8; 428 us of 512
-  // heads with 1, 354 with 8 (both kernels).
+  // of them once: as many as leave 4 waves a SIMD.  8 value heads a key head, us
+  // of this kernel: 8 sequences of up to 4096 tokens, 64 heads, 118 with 8 in a
+  // wave, 152 with 2, 194 with 1; 2048 tokens, 32 heads, 23 with 8, 13 with 1.
   const int per = (int)std::min<int64_t>(p.hpg, std::max<int64_t>(1, chunks * p.Hv / 4096));
   const int waves = (p.hpg + per - 1) / per;
   const int64_t ntiles = chunks * p.Hk * waves;
