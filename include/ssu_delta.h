@@ -13,8 +13,8 @@
  *   o_t = scale S q^_t
  * Everything between the inputs and the outputs is computed in fp32 (decay
  * sums in fp64); matrix products take operands that are not bf16 in two or
- * three bf16 parts: fp32 states and a step's fp32 outputs end about 1e-6 of
- * their norm or less from the exact ones, a prompt's fp32 outputs 5e-6.
+ * three bf16 parts: fp32 states and fp32 outputs end about 1e-6 of their norm
+ * or less from the exact ones.
  * Infinities or NaN in a token's inputs may reach every output of the call for
  * its request and head (the tokens before it in the call too), and nothing
  * else.

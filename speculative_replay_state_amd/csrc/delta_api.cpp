@@ -168,7 +168,7 @@ int check_prefill_sizes(int64_t rows, int64_t n, int64_t hv) {
 }
 
 size_t prefill_bytes(int64_t rows, int64_t n, int64_t hv) {
-  return (size_t)((rows / ssu::kChunk + n) * hv * ssu::kRecBytes);
+  return (size_t)((rows / ssu::kChunk + n) * hv * ssu::kRecMax);
 }
 
 }  // namespace

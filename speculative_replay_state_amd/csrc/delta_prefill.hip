@@ -11,9 +11,11 @@
 // are few and each chunk's latency adds up.  Products with q, k and v take them
 // as they are (bf16); the state enters the products with k and q in two bf16
 // parts, R the one with T - I in two (T - I too; the identity's share of U is
-// R in fp32), U the update in three and the outputs in two.  Against 64 bits,
-// fp32 states end 3e-7 to 8e-7 of their norm off, fp32 outputs 4e-6; with T R in
-// fp32 products the states 1e-7 to 2e-7, and the calls below 622 and 511 us.
+// R in fp32), U the update in three and, with P, the outputs in two, or three
+// where they are fp32.  Against 64 bits, fp32 states end 3e-7 to 8e-7 of their
+// norm off, fp32 outputs 7e-7 to 1.1e-6 (with two parts 4e-6, for 691 us where
+// three take 742); with T R in fp32 products the states 1e-7 to 2e-7, and the
+// calls below 622 and 511 us.
 //
 // What bounds them, at 8 sequences of 2048 to 4096 tokens with 64 heads of dim
 // 128, 600 us: the chunk kernel takes 118 us (0.32 GB of records written), the
@@ -56,30 +58,35 @@ __device__ __forceinline__ bool seq_rows(const DPrefill &p, int s, int &b0, int 
   return b0 >= 0 && b0 <= b1 && b1 <= p.rows;
 }
 
-// Rows 16 ti .. of a 32 x 32 lower triangle as row operands of two bf16 parts,
+// Parts of P and U in their product.
+constexpr int out_parts(int OT) { return OT == kOutF32 ? 3 : 2; }
+
+// Rows 16 ti .. of a 32 x 32 lower triangle as row operands of NP bf16 parts,
 // [part][lane]; the first 16 rows are half as long.
+template <int NP>
 __device__ __forceinline__ void write_rows(uint8_t *at, int ti, int lane, const float (&x)[8]) {
-  bf16x8 f[2];
-  split<2>(x, f);
+  bf16x8 f[NP];
+  split<NP>(x, f);
 #pragma unroll
-  for (int a = 0; a < 2; ++a) {
+  for (int a = 0; a < NP; ++a) {
     const u32x4 v = __builtin_bit_cast(u32x4, f[a]);
     if (ti == 0)
       st8(at + (a * 64 + lane) * 8, u32x2{v[0], v[1]});
     else
-      st16(at + 2 * 64 * 8 + (a * 64 + lane) * 16, v);
+      st16(at + NP * 64 * 8 + (a * 64 + lane) * 16, v);
   }
 }
 // A row operand of them, part a; the first 16 rows' in the lower half.
 __device__ __forceinline__ u32x2 short_row(const uint8_t *at, int a, int lane) { return ld8(at + (a * 64 + lane) * 8); }
+template <int NP>
 __device__ __forceinline__ bf16x8 long_row(const uint8_t *at, int a, int lane) {
-  return __builtin_bit_cast(bf16x8, ld16(at + 2 * 64 * 8 + (a * 64 + lane) * 16));
+  return __builtin_bit_cast(bf16x8, ld16(at + NP * 64 * 8 + (a * 64 + lane) * 16));
 }
 __device__ __forceinline__ bf16x8 halves(u32x2 a, u32x2 b) { return __builtin_bit_cast(bf16x8, u32x4{a[0], a[1], b[0], b[1]}); }
 
 // A wave takes a chunk of one key head: k . k and k . q once, then T and P of
 // `per` of the value heads that share it.
-template <int DK>
+template <int DK, int NP>
 __global__ __launch_bounds__(64, 3) void delta_chunk_kernel(DPrefill p, int per, int waves, int64_t ntiles) {
   __shared__ WinLds<kChunk> w;
   __shared__ __align__(16) float rq[kChunk];
@@ -152,7 +159,7 @@ __global__ __launch_bounds__(64, 3) void delta_chunk_kernel(DPrefill p, int per,
     wave_sync();
     f32x4 decay[3];
     write_A<kChunk>(w, m, q, kk, decay);
-    uint8_t *rec = p.ws + ((int64_t)slot * p.Hv + h) * kRecBytes;
+    uint8_t *rec = p.ws + ((int64_t)slot * p.Hv + h) * rec_bytes(NP);
 #pragma unroll
     for (int ti = 0; ti < 2; ++ti) {
       const int i = 16 * ti + m;
@@ -163,7 +170,7 @@ __global__ __launch_bounds__(64, 3) void delta_chunk_kernel(DPrefill p, int per,
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           x[4 * a + e] = a <= ti && 16 * a + 4 * q + e <= i ? r * decay[a <= ti ? ti + a : 0][e] * qk[a <= ti ? ti + a : 0][e] : 0.f;
-      write_rows(rec + kRecT, ti, lane, x);
+      write_rows<NP>(rec + kRecT + kRecF, ti, lane, x);
     }
     wave_sync();
     invert_diag<kChunk>(w, lane);
@@ -173,9 +180,9 @@ __global__ __launch_bounds__(64, 3) void delta_chunk_kernel(DPrefill p, int per,
       t_row<kChunk>(w, ti, m, q, x);
 #pragma unroll
       for (int e = 0; e < 4; ++e) x[4 * ti + e] = 4 * q + e == m ? 0.f : x[4 * ti + e];  // T - I
-      write_rows(rec, ti, lane, x);
+      write_rows<2>(rec, ti, lane, x);
     }
-    float *f = reinterpret_cast<float *>(rec + kRecT + kRecP);
+    float *f = reinterpret_cast<float *>(rec + kRecT);
     if (lane < kChunk) {
       const double Gw = w.G[kChunk - 1];
       const float e = exp2_d(G), rk = w.rk[lane];
@@ -194,12 +201,13 @@ constexpr int pieces(int n, int NT) { return (n + NT - 1) / NT; }
 // What the waves of a chain share of a chunk.  (Rows that avoid the bank
 // conflicts of the transposed reads, 16 banks apart instead of 4, halve those
 // conflicts and change no time: 622 us either way for the 8 sequences below.)
-template <int DK, int COLS>
+template <int DK, int COLS, int NP>
 struct Chunk {
+  static constexpr int kRec = rec_bytes(NP);
   static constexpr int KS = DK + 8, VS = COLS + 8;  // row strides: 16 rows start in different banks
   __align__(16) uint16_t k[kChunk * KS], q[kChunk * KS], v[kChunk * VS];
-  __align__(16) uint8_t rec[kRecBytes];
-  __device__ __forceinline__ const float *factors() const { return reinterpret_cast<const float *>(rec + kRecT + kRecP); }
+  __align__(16) uint8_t rec[kRec];
+  __device__ __forceinline__ const float *factors() const { return reinterpret_cast<const float *>(rec + kRecT); }
 };
 
 // One sequence's chunks of a head's columns c0 .. c0 + COLS - 1.
@@ -212,10 +220,9 @@ struct Chain {
 // exactly: behind the sequence's end (and the last chunk) they repeat its last
 // row (and chunk), whose gates in the record are 0, and columns behind dim_v
 // repeat the first ones.
-template <int DK, int COLS, int NT>
+template <class Buf, int DK, int COLS, int NT>
 struct Stage {
-  typedef Chunk<DK, COLS> Buf;
-  static constexpr int PK = pieces(kChunk * DK / 8, NT), PV = pieces(kChunk * COLS / 8, NT), PR = pieces(kRecBytes / 16, NT);
+  static constexpr int PK = pieces(kChunk * DK / 8, NT), PV = pieces(kChunk * COLS / 8, NT), PR = pieces(Buf::kRec / 16, NT);
   u32x4 k[PK], q[PK], v[PV], r[PR];
 
   __device__ __forceinline__ void fetch(const DPrefill &p, const Chain &n, const uint8_t *rec0, int c, int tid) {
@@ -227,7 +234,7 @@ struct Stage {
     const char *kc = reinterpret_cast<const char *>(p.k + row * p.k_stride + hk * DK);
     const char *qc = reinterpret_cast<const char *>(p.q + row * p.q_stride + hk * DK);
     const char *vc = reinterpret_cast<const char *>(p.v + row * p.v_stride + n.h * p.dv + n.c0);
-    const uint8_t *rec = rec0 + (int64_t)c * p.Hv * kRecBytes;
+    const uint8_t *rec = rec0 + (int64_t)c * p.Hv * Buf::kRec;
 #pragma unroll
     for (int i = 0; i < PK; ++i) {
       const int at = i * NT + tid, t = min(at / (DK / 8), last), ch = at % (DK / 8);
@@ -240,7 +247,7 @@ struct Stage {
       v[i] = ld16(vc + (uint32_t)(t * vs + (n.c0 + ch * 8 < p.dv ? ch * 16 : 0)));
     }
 #pragma unroll
-    for (int i = 0; i < PR; ++i) r[i] = ld16(rec + (uint32_t)(min(i * NT + tid, kRecBytes / 16 - 1) * 16));
+    for (int i = 0; i < PR; ++i) r[i] = ld16(rec + (uint32_t)(min(i * NT + tid, Buf::kRec / 16 - 1) * 16));
   }
 
   // (a thread without a piece of its own writes the last one again)
@@ -257,7 +264,7 @@ struct Stage {
       st16(o.v + t * Buf::VS + ch * 8, v[i]);
     }
 #pragma unroll
-    for (int i = 0; i < PR; ++i) st16(o.rec + min(i * NT + tid, kRecBytes / 16 - 1) * 16, r[i]);
+    for (int i = 0; i < PR; ++i) st16(o.rec + min(i * NT + tid, Buf::kRec / 16 - 1) * 16, r[i]);
   }
 };
 
@@ -278,20 +285,20 @@ __device__ __forceinline__ bf16x8 row_tile(const uint16_t *rows, int n0, int ti,
 }
 
 // What a chunk's residuals and update take from LDS beside k.
-template <int DK, int COLS>
 struct Factors {
   u32x2 ts[2];  // T's rows in two parts
   bf16x8 tl[2];
   f32x4 b[2], be[2], e[2];  // b, b e^G / |k|, e^(G_w - G) / |k| of the lane's tokens
   s16x4 v[2];
   float ew;
-  __device__ __forceinline__ void load_residual(const Chunk<DK, COLS> &in, int block, int lane) {
+  template <class Buf>
+  __device__ __forceinline__ void load_residual(const Buf &in, int block, int lane) {
     const int m = lane & 15, q = lane >> 4;
     const float *fac = in.factors();
 #pragma unroll
     for (int a = 0; a < 2; ++a) {
       ts[a] = short_row(in.rec, a, lane);
-      tl[a] = long_row(in.rec, a, lane);
+      tl[a] = long_row<2>(in.rec, a, lane);
     }
 #pragma unroll
     for (int ti = 0; ti < 2; ++ti) {
@@ -300,7 +307,8 @@ struct Factors {
       v[ti] = lds_tr4(in.v + (16 * ti + 4 * q + (m >> 2)) * in.VS + block * 16 + 4 * (m & 3));
     }
   }
-  __device__ __forceinline__ void load_update(const Chunk<DK, COLS> &in, int lane) {
+  template <class Buf>
+  __device__ __forceinline__ void load_update(const Buf &in, int lane) {
     const float *fac = in.factors();
 #pragma unroll
     for (int ti = 0; ti < 2; ++ti) e[ti] = *reinterpret_cast<const f32x4 *>(fac + 64 + 16 * ti + 4 * (lane >> 4));
@@ -334,8 +342,8 @@ struct Factors {
 };
 
 // k transposed: tokens along the depth; row m = 4 j + r of the tile is n = n0 + 8 j + 4 a + r
-template <int DK, int COLS>
-__device__ __forceinline__ bf16x8 key_tile(const Chunk<DK, COLS> &in, int n0, int a, int lane) {
+template <class Buf>
+__device__ __forceinline__ bf16x8 key_tile(const Buf &in, int n0, int a, int lane) {
   const int m = lane & 15, q = lane >> 4;
   const uint16_t *at = in.k + (4 * q + (m >> 2)) * in.KS + n0 + 8 * (m & 3) + 4 * a;
   struct { s16x4 lo, hi; } kt = {lds_tr4(at), lds_tr4(at + 16 * in.KS)};
@@ -346,17 +354,19 @@ __device__ __forceinline__ bf16x8 key_tile(const Chunk<DK, COLS> &in, int n0, in
 // Q S^T.  Rows behind the sequence, columns behind dim_v and waves that have
 // nothing to write (!on) go past the buffer's end, where the hardware drops
 // them: a branch around the store would cost the loop its exact waits.
-template <int OT, int DK, int COLS>
-__device__ __forceinline__ void write_outputs(const DPrefill &p, const Chain &n, const Chunk<DK, COLS> &in, int c, int ti, int col,
-                                              bool on, int lane, const bf16x8 (&fu)[2], f32x4 o) {
+template <int OT, class Buf>
+__device__ __forceinline__ void write_outputs(const DPrefill &p, const Chain &n, const Buf &in, int c, int ti, int col, bool on,
+                                              int lane, const bf16x8 (&fu)[out_parts(OT)], f32x4 o) {
   const int m = lane & 15, q = lane >> 4;
   constexpr int kOut = OT == kOutF32 ? 4 : 2;
   const int row0 = n.b0 + c * kChunk, rows = min(kChunk, n.b1 - row0), row_bytes = p.Hv * p.dv * kOut;
   const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(static_cast<uint8_t *>(p.out) + (int64_t)row0 * row_bytes, 0,
                                                       rows * row_bytes, 0x00020000);
-  bf16x8 f[2];
+  constexpr int NP = out_parts(OT);
+  const uint8_t *P = in.rec + kRecT + kRecF;
+  bf16x8 f[NP];
 #pragma unroll
-  for (int a = 0; a < 2; ++a) f[a] = ti == 0 ? halves(short_row(in.rec + kRecT, a, lane), u32x2{0, 0}) : long_row(in.rec + kRecT, a, lane);
+  for (int a = 0; a < NP; ++a) f[a] = ti == 0 ? halves(short_row(P, a, lane), u32x2{0, 0}) : long_row<NP>(P, a, lane);
   const int t = 16 * ti + m;
   o = mfma_parts(fu, f, scale4(o, in.factors()[96 + t]));
   const int at = t < rows && col < p.dv && on ? t * row_bytes + (n.h * p.dv + col + 4 * q) * kOut : 0x7FFFFFF0;
@@ -366,9 +376,10 @@ __device__ __forceinline__ void write_outputs(const DPrefill &p, const Chain &n,
     __builtin_amdgcn_raw_buffer_store_b64(u32x2{pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3])}, rsrc, at, 0, 0);
 }
 
-__device__ __forceinline__ void split_u(const f32x4 (&U)[2], bf16x8 (&fu)[2]) {
+template <int NP>
+__device__ __forceinline__ void split_u(const f32x4 (&U)[2], bf16x8 (&fu)[NP]) {
   const float y[8] = {U[0][0], U[0][1], U[0][2], U[0][3], U[1][0], U[1][1], U[1][2], U[1][3]};
-  split<2>(y, fu);
+  split<NP>(y, fu);
 }
 
 // The lane's rows of the state from and to the fp32 states of a sequence.
@@ -451,11 +462,15 @@ inline dim3 chain_grid(const DPrefill &p, int groups, int unit) {
 // registers, with one barrier a chunk: behind it everyone has read chunk c - 1.
 // LDS reads bound a lone workgroup and its waves wait at the same places, so
 // two workgroups share a CU (8 sequences of 2048 to 4096 tokens, 64 heads of
-// dim 128: 800 us with one and three buffers, 691 with two).
+// dim 128: 800 us with one and three buffers, 691 with two).  The bf16 form fits
+// the 128 registers of that by itself; the fp32 form of whole heads is held to
+// them, which spills a few (742 us for 3000 tokens each; 771 with 166 registers
+// and one workgroup).
 template <int OT, int DK, int NC>
-__global__ __launch_bounds__(NC * 64, 2) void delta_scan_kernel(DPrefill p, int groups, int unit) {
-  constexpr int COLS = NC * 16, NK = DK / 32;
-  __shared__ Chunk<DK, COLS> buf[2];
+__global__ __launch_bounds__(NC * 64, OT == kOutF32 ? NC / 2 : 2) void delta_scan_kernel(DPrefill p, int groups, int unit) {
+  constexpr int COLS = NC * 16, NK = DK / 32, NP = out_parts(OT);
+  typedef Chunk<DK, COLS, NP> Buf;
+  __shared__ Buf buf[2];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, m = lane & 15, q = lane >> 4;
   Chain n;
   int seq;
@@ -465,13 +480,13 @@ __global__ __launch_bounds__(NC * 64, 2) void delta_scan_kernel(DPrefill p, int 
   const int64_t state = (((int64_t)seq * p.Hv + n.h) * p.dv + col + m) * DK + 8 * q;
   load_state(p.h0, state, col < p.dv, S);
   if (n.chunks > 0) {
-    const uint8_t *rec0 = p.ws + ((int64_t)chunk_base(p, seq) * p.Hv + n.h) * kRecBytes;
-    Stage<DK, COLS, NC * 64> st;
+    const uint8_t *rec0 = p.ws + ((int64_t)chunk_base(p, seq) * p.Hv + n.h) * Buf::kRec;
+    Stage<Buf, DK, COLS, NC * 64> st;
     st.fetch(p, n, rec0, 0, tid);
     st.store(buf[0], tid);
     st.fetch(p, n, rec0, 1, tid);
     for (int c = 0; c < n.chunks; ++c) {
-      const Chunk<DK, COLS> &in = buf[c & 1];
+      const Buf &in = buf[c & 1];
       __syncthreads();
       st.store(buf[(c + 1) & 1], tid);
       st.fetch(p, n, rec0, c + 2, tid);
@@ -495,19 +510,19 @@ __global__ __launch_bounds__(NC * 64, 2) void delta_scan_kernel(DPrefill p, int 
             o[ti] = mfma_bf16(fs[a], qf[ti], o[ti]);
           }
       }
-      Factors<DK, COLS> fac;
+      Factors fac;
       fac.load_residual(in, wave, lane);
       fac.residuals(x, U);
       // S <- e^(G_w) S + (e^(G_w - G) U / |k|)^T K
       fac.load_update(in, lane);
-      bf16x8 fw[3], fu[2];
+      bf16x8 fw[3], fu[NP];
       fac.update(U, fw);
 #pragma unroll
       for (int i = 0; i < NK; ++i)
 #pragma unroll
         for (int a = 0; a < 2; ++a)
           S[i][a] = Tok<32>::exact<true>(key_tile(in, 32 * i, a, lane), fw, scale4(S[i][a], fac.ew));
-      split_u(U, fu);
+      split_u<NP>(U, fu);
 #pragma unroll
       for (int ti = 0; ti < 2; ++ti) write_outputs<OT>(p, n, in, c, ti, col, true, lane, fu, o[ti]);
     }
@@ -527,14 +542,14 @@ __global__ __launch_bounds__(NC * 64, 2) void delta_scan_kernel(DPrefill p, int 
 template <int OT, int DK>
 __global__ __launch_bounds__(6 * 64, 1) void delta_chain_kernel(DPrefill p, int groups, int unit) {
   constexpr int NS = 2, NH = 4, NK = DK / 32 / NS;
-  typedef Chunk<DK, 16> Buf;
+  typedef Chunk<DK, 16, out_parts(OT)> Buf;
   __shared__ Buf buf[4];
   __shared__ f32x4 red_x[2][NS][2][64], red_o[2][NS][2][64], shared_u[2][2][64];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, m = lane & 15, q = lane >> 4;
   Chain n;
   int seq;
   if (!chain_of<16>(p, groups, unit, n, seq)) return;
-  const uint8_t *rec0 = p.ws + ((int64_t)chunk_base(p, seq) * p.Hv + n.h) * kRecBytes;
+  const uint8_t *rec0 = p.ws + ((int64_t)chunk_base(p, seq) * p.Hv + n.h) * Buf::kRec;
   if (wave < NS) {
     const int n0 = wave * NK * 32;
     f32x4 S[NK][2];
@@ -545,7 +560,7 @@ __global__ __launch_bounds__(6 * 64, 1) void delta_chain_kernel(DPrefill p, int 
       __syncthreads();
       struct Held {
         bf16x8 k[NK][2], q[NK][2], kt[NK][2];
-        Factors<DK, 16> fac;
+        Factors fac;
       };
       auto hold = [&](int c, Held &h) {
         const Buf &in = buf[c & 3];
@@ -618,14 +633,14 @@ __global__ __launch_bounds__(6 * 64, 1) void delta_chain_kernel(DPrefill p, int 
 #pragma unroll
       for (int w = 1; w < NS; ++w) o += red_o[c & 1][w][hw & 1][lane];
       const f32x4 U[2] = {shared_u[c & 1][0][lane], shared_u[c & 1][1][lane]};
-      bf16x8 fu[2];
-      split_u(U, fu);
+      bf16x8 fu[out_parts(OT)];
+      split_u<out_parts(OT)>(U, fu);
       write_outputs<OT>(p, n, buf[c & 3], c, hw & 1, n.c0, hw < 2, lane, fu, o);
     };
     // chunk c + SETS is fetched while c + 1 is stored: as many register sets, so
     // that a chunk has several iterations to arrive
     constexpr int SETS = 4;
-    Stage<DK, 16, NH * 64> st[SETS];
+    Stage<Buf, DK, 16, NH * 64> st[SETS];
 #pragma unroll
     for (int i = 0; i < SETS; ++i) st[i].fetch(p, n, rec0, i, ht);
     st[0].store(buf[0], ht);
@@ -678,7 +693,10 @@ hipError_t prefill_dk(const DPrefill &p, int out_type, hipStream_t st) {
   const int per = (int)std::min<int64_t>(p.hpg, std::max<int64_t>(1, chunks * p.Hv / 4096));
   const int waves = (p.hpg + per - 1) / per;
   const int64_t ntiles = chunks * p.Hk * waves;
-  delta_chunk_kernel<DK><<<dim3(xcd_grid(ntiles)), dim3(64), 0, st>>>(p, per, waves, ntiles);
+  if (out_type == kOutF32)
+    delta_chunk_kernel<DK, out_parts(kOutF32)><<<dim3(xcd_grid(ntiles)), dim3(64), 0, st>>>(p, per, waves, ntiles);
+  else
+    delta_chunk_kernel<DK, out_parts(kOutBF16)><<<dim3(xcd_grid(ntiles)), dim3(64), 0, st>>>(p, per, waves, ntiles);
   const hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;
   // Few chains: a workgroup to a block of 16 columns while each gets a CU of its
