@@ -8,6 +8,7 @@ import shutil
 import subprocess
 
 import pytest
+import torch  # noqa: F401  (before the library, which then shares torch's HIP runtime instead of loading a second one)
 
 import speculative_replay_state_amd as ssu
 from speculative_replay_state_amd import delta, verification
