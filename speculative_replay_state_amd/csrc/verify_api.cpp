@@ -95,7 +95,6 @@ int ssu_verify(const ssu_verify_args *a, hipStream_t stream) {
   v.next_left = a->next_left;
   v.ws = static_cast<double *>(a->workspace);
   v.status = a->status;
-  v.wide = aligned(v.p, 16) && v.p_stride % 16 == 0 && (!v.q || (aligned(v.q, 16) && v.q_stride % 16 == 0));
   const hipError_t err = ssu::launch_verify(v, pt == SSU_F32 ? ssu::kPF32 : (pt == SSU_BF16 ? ssu::kPBF16 : ssu::kPF16), stream);
   return err == hipSuccess ? api_ok() : api_fail(SSU_ERR_HIP, "kernel launch failed: %s", hipGetErrorString(err));
 }

@@ -31,7 +31,6 @@ struct KVerify {
   int32_t *next_live, *next_fold, *next_left;
   double *ws;                    // [batch][verify_words]
   int32_t *status;
-  int wide;                      // rows can be read 16 bytes at a time
 };
 
 hipError_t launch_verify(const KVerify &v, int prob_type, hipStream_t stream);

@@ -10,9 +10,10 @@
 //
 // What bounds them is one read of row n of both distributions, behind the
 // drafts' own (dependent) reads.  256 entries of 8 tokens, 131072 bf16 values in
-// two distributions: 27.9 us, 4.8 TB/s (32.1 in two launches); 64 entries,
+// two distributions: 27.1 us, 4.9 TB/s (32.1 in two launches); 64 entries,
 // 100003 fp32 values without draft probabilities (rows no 16 bytes apart):
-// 13.1 us; one entry of 32000: 8.7 us.  With four pieces a wave of
+// 12.7 us (13.5 with those rows read 4 bytes a lane); one entry of 32000: 7.8
+// us.  With four pieces a wave of
 // verify_sum_kernel 36.7, 14.9 and 10.5 us, with one 32.4, 13.1 and 8.9 (fewer
 // waves wait for their drafts); with the verdicts in a kernel of their own
 // 31.6, 15.2, 11.9.
@@ -35,14 +36,16 @@ __device__ __forceinline__ float prob_at(const uint8_t *row, int i) {
   return (float)__builtin_bit_cast(_Float16, v);
 }
 
-// Eight neighbouring values as they are in memory, from 16-byte aligned pieces.
+// Eight neighbouring values as they are in memory, 16 bytes at a time from
+// wherever the row starts (global loads need no alignment).
+typedef u32x4 u32x4_any __attribute__((aligned(2)));
 template <int PT>
 struct Eight {
   u32x4 w[PT == kPF32 ? 2 : 1];
   __device__ __forceinline__ void load(const uint8_t *row, int i) {
     const uint8_t *at = row + (int64_t)i * (PT == kPF32 ? 4 : 2);
-    w[0] = ld16(at);
-    if constexpr (PT == kPF32) w[1] = ld16(at + 16);
+    w[0] = *reinterpret_cast<const u32x4_any *>(at);
+    if constexpr (PT == kPF32) w[1] = *reinterpret_cast<const u32x4_any *>(at + 16);
   }
   __device__ __forceinline__ float value(int k) const {
     if constexpr (PT == kPF32) return __uint_as_float(w[k / 4][k % 4]);
@@ -106,9 +109,9 @@ __device__ __forceinline__ double wave_sum(double x) {
 }
 
 // Sum of r over a piece, in every lane, with every load in flight before the
-// first is used.  WIDE (rows of 16-byte pieces, this one within the
-// vocabulary): 8 neighbours a lane and load; else a value a lane, 64 neighbours
-// a load, and past the vocabulary its last value, not counted.
+// first is used.  WIDE (a piece within the vocabulary): 8 neighbours a lane and
+// load; else a value a lane, 64 neighbours a load, and past the vocabulary its
+// last value, not counted.
 template <int PT, bool WIDE>
 __device__ __forceinline__ double piece_sum(const KVerify &v, const Verdict &o, bool rejected, int piece, int lane) {
   const int64_t row = (int64_t)o.bos + o.n;
@@ -173,7 +176,7 @@ __global__ __launch_bounds__(kSumWaves * 64) void verify_sum_kernel(KVerify v, i
   if (piece == 0 && lane == 0) write_verdict(o, ws, pieces);
   if (o.T <= 0) return;
   const bool rejected = o.n < o.T - 1 && o.draft >= 0;
-  const double sum = v.wide && (piece + 1) * kVerifyPiece <= v.vocab ? piece_sum<PT, true>(v, o, rejected, piece, lane)
+  const double sum = (piece + 1) * kVerifyPiece <= v.vocab ? piece_sum<PT, true>(v, o, rejected, piece, lane)
                                                                      : piece_sum<PT, false>(v, o, rejected, piece, lane);
   if (lane == 0) ws[piece] = sum;
 }
@@ -251,14 +254,29 @@ __device__ __forceinline__ void pick(const KVerify &v, const Verdict &o, double 
       const uint8_t *p = v.p + row * v.p_stride, *q = rejected && v.q ? v.q + row * v.q_stride : p;
       const int i0 = piece * kVerifyPiece + lane * kLane;
       float r[kLane], less[kLane];
+      if ((piece + 1) * kVerifyPiece <= v.vocab) {
+        Eight<PT> a[kLane / 8], c[kLane / 8];
 #pragma unroll
-      for (int i = 0; i < kLane; ++i) r[i] = prob_at<PT>(p, min(i0 + i, v.vocab - 1));
+        for (int k = 0; k < kLane / 8; ++k) {
+          a[k].load(p, i0 + 8 * k);
+          c[k].load(q, i0 + 8 * k);
+        }
 #pragma unroll
-      for (int i = 0; i < kLane; ++i) less[i] = prob_at<PT>(q, min(i0 + i, v.vocab - 1));
+        for (int i = 0; i < kLane; ++i) {
+          r[i] = a[i / 8].value(i % 8);
+          less[i] = c[i / 8].value(i % 8);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < kLane; ++i) {
+          r[i] = prob_at<PT>(p, min(i0 + i, v.vocab - 1));
+          less[i] = prob_at<PT>(q, min(i0 + i, v.vocab - 1));
+        }
+      }
       double mine = 0.0;
 #pragma unroll
       for (int i = 0; i < kLane; ++i) {
-        if (rejected) r[i] -= q != p ? less[i] : (i0 + i == o.draft ? 1.f : 0.f);
+        if (rejected) r[i] -= v.q ? less[i] : (i0 + i == o.draft ? 1.f : 0.f);
         r[i] = i0 + i < v.vocab ? positive(r[i]) : 0.f;
         mine += (double)r[i];
       }
@@ -314,7 +332,7 @@ __global__ __launch_bounds__(kRowWaves * 64) void verify_row_kernel(KVerify v, i
   if (o.T > 0) {
     const bool rejected = o.n < o.T - 1 && o.draft >= 0;
     for (int k = wave; k < pieces; k += kRowWaves) {
-      const double sum = v.wide && (k + 1) * kVerifyPiece <= v.vocab ? piece_sum<PT, true>(v, o, rejected, k, lane)
+      const double sum = (k + 1) * kVerifyPiece <= v.vocab ? piece_sum<PT, true>(v, o, rejected, k, lane)
                                                                      : piece_sum<PT, false>(v, o, rejected, k, lane);
       if (lane == 0) sums[k] = sum;
     }
