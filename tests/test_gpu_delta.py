@@ -372,10 +372,11 @@ def test_prefill(lens, hk, hv, dk, dv, init, out_name):
 
 # the chains (sequence, value head) that each scan kernel takes: up to 256 blocks of 16 columns one kernel, more another,
 # over 256 chains of more than 64 columns a third
+@pytest.mark.parametrize("out_name", ["bf16", "f32"])
 @pytest.mark.parametrize("n,most,hk,hv,dk,dv,init", [(9, 70, 2, 4, 128, 128, True), (20, 90, 4, 8, 64, 64, True),
                                                      (20, 100, 2, 8, 128, 48, False), (40, 100, 4, 8, 128, 128, True),
                                                      (33, 66, 2, 8, 64, 144, False), (64, 40, 1, 4, 64, 256, True)])
-def test_prefill_of_many_chains(n, most, hk, hv, dk, dv, init):
+def test_prefill_of_many_chains(n, most, hk, hv, dk, dv, init, out_name):
     g = gen(n + dv)
     lens = torch.randint(0, most + 1, (n,), generator=g).tolist()
     lens[:3] = [most, 0, 33]
@@ -386,7 +387,7 @@ def test_prefill_of_many_chains(n, most, hk, hv, dk, dv, init):
     x["k"][cu[-1]:] = float("nan")
     h0 = 0.3 * torch.randn(n, hv, dv, dk, generator=g) if init else None
     h1 = torch.empty(n, hv, dv, dk, device=DEV)
-    out = torch.full((cu[-1] + 3, hv, dv), 7.0, dtype=torch.float32, device=DEV)
+    out = torch.full((cu[-1] + 3, hv, dv), 7.0, dtype=R.TYPES[out_name], device=DEV)
     print("chains", n * hv, dk, dv, flush=True)
     call_prefill(up(x), cu, out, None if h0 is None else h0.to(DEV), h1)
     o, gt, h1 = out.cpu(), R.gates(x["dt"], x["beta"], x["A"], x["dt_bias"]), h1.cpu()
@@ -397,7 +398,7 @@ def test_prefill_of_many_chains(n, most, hk, hv, dk, dv, init):
         S, want = R.run(S0, x["q"][at], x["k"][at], x["v"][at], gt[0][at], gt[1][at], dk ** -0.5)
         went = S0.double().flatten(1).norm(dim=1) + x["v"][at].double().transpose(0, 1).flatten(1).norm(dim=1)
         windows = max(1, -(-lens[s] // 32))
-        R.check(o[at].transpose(0, 1), want.transpose(0, 1), went * dk ** -0.5, R.tol(dk, 32, windows, "f32"), "outputs %d" % s)
+        R.check(o[at].transpose(0, 1), want.transpose(0, 1), went * dk ** -0.5, R.tol(dk, 32, windows, out_name), "outputs %d" % s)
         R.check(h1[s], S, went, R.tol(dk, 32, windows, "f32"), "state %d" % s)
 
 
@@ -540,3 +541,20 @@ def test_slots_past_4_gib():
     for j, slot in enumerate(ids):
         assert torch.equal(state[slot], d["state"][j + 1])
     assert not bool(state[:8].any()) and not bool(state[slots - 10:slots - 2].any())
+
+
+def test_prompt_rows_past_4_gib():
+    """Sequences whose rows of v, out and the scratch lie past 2^32 bytes, bit for bit as at the front."""
+    g = gen(18)
+    rows, hk, hv = 140000, 2, 128
+    x = up(R.inputs(g, 300, hk, hv, 64, 128))
+    far = {n: torch.zeros(rows, *x[n].shape[1:], dtype=x[n].dtype, device=DEV) for n in ("q", "k", "v", "dt", "beta")}
+    for n in far:
+        far[n][-300:] = x[n]
+    far["A"], far["dt_bias"] = x["A"], x["dt_bias"]
+    out, want = torch.zeros(rows, hv, 128, dtype=torch.bfloat16, device=DEV), torch.empty(300, hv, 128, dtype=torch.bfloat16, device=DEV)
+    h1, w1 = torch.empty(2, hv, 128, 64, device=DEV), torch.empty(2, hv, 128, 64, device=DEV)
+    print("prompt rows past 4 GiB", flush=True)
+    call_prefill(far, [rows - 300, rows - 100, rows], out, None, h1)
+    call_prefill(x, [0, 200, 300], want, None, w1)
+    assert torch.equal(out[-300:], want) and torch.equal(h1, w1) and not bool(out[:100].any())

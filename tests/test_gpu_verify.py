@@ -250,3 +250,27 @@ def test_drawn_tokens_follow_the_target():
     out, _, _ = run(tokens, np.tile(p, (2 * n, 1)), np.tile(q, (2 * n, 1)), rng.random(2 * n), rng.random(n), 2)
     freq = np.bincount(out[:, 0], minlength=5) / n
     assert np.all(np.abs(freq - p) <= 5 * np.sqrt(p * (1 - p) / n)), freq
+
+
+def test_rows_past_4_gib():
+    """Probability rows past 2^32 bytes, as at the front."""
+    vocab, rows = 131072, 8400
+    g = torch.Generator(device=DEV)
+    g.manual_seed(7)
+    few = torch.softmax(torch.randn(8, vocab, generator=g, device=DEV), -1)
+    far = torch.zeros(rows, vocab, device=DEV)
+    far[-8:] = few
+    tokens, u, uf = [5, 77] * 4, [0.0, 0.5] * 4, [0.1, 0.4, 0.6, 0.9]
+    print("rows past 4 GiB", flush=True)
+
+    def call(p, cu):
+        n = p.shape[0]
+        pad = lambda x, dt: torch.cat([torch.zeros(n - 8, dtype=dt), torch.tensor(x, dtype=dt)]).to(DEV)  # noqa: E731
+        out, acc = torch.empty(4, 2, dtype=torch.int32, device=DEV), torch.empty(4, dtype=torch.int32, device=DEV)
+        ws = torch.empty(ssu.verify_workspace_size(4, vocab), dtype=torch.uint8, device=DEV)
+        ssu.verify(ssu.make_verify(pad(tokens, torch.int32), p, None, pad(u, torch.float32), torch.tensor(uf, device=DEV), out, acc, ws,
+                                   torch.tensor(cu, dtype=torch.int32, device=DEV)))
+        return out.tolist(), acc.tolist()
+
+    want = call(few, [0, 2, 4, 6, 8])
+    assert call(far, [rows - 8, rows - 6, rows - 4, rows - 2, rows]) == want and min(want[0][0]) >= 0
