@@ -193,6 +193,35 @@ def test_loops_interleaved_on_streams_of_their_own():
         assert all(torch.equal(a, b) for a, b in zip(l.results(), w))
 
 
+def test_two_graphs_replayed_at_once():
+    """Two captured loops, caches and scratch of their own, replayed on two streams without a wait between them."""
+    loops = [Loop(11, batch=6, L=16, state="bf16", dk=128), Loop(12, batch=9, L=32, steps=5, state="f32")]
+    graphs, want = [], []
+    for l in loops:
+        l.build()
+        l.reset()
+        l.run()
+        torch.cuda.synchronize()
+        want.append([t.clone() for t in l.results()])
+        l.reset()
+        torch.cuda.synchronize()
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1], stream=torch.cuda.Stream()):
+            l.run()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(4):
+        for l in loops:
+            for t in l.results():
+                t.zero_()
+        torch.cuda.synchronize()
+        for graph, stream in zip(graphs, streams):
+            with torch.cuda.stream(stream):
+                graph.replay()
+        torch.cuda.synchronize()
+        for l, w in zip(loops, want):
+            assert all(torch.equal(a, b) for a, b in zip(l.results(), w))
+
+
 def test_verification_drives_the_selective_state_update():
     """next_live and next_fold are the prev_num_accepted and num_fold of the next fused ssu step: a loop of them
     equals steps and flushes whose counts the host keeps."""
