@@ -2,10 +2,10 @@
 // (one instantiation per checkpoint type).
 //
 // Both are bound by HBM, the checkpoint read once (and written once): 64
-// entries of 64 heads of 128 x 128, 4 new tokens, bf16, 33.8 us = 4.5 TB/s; 256
+// entries of 64 heads of 128 x 128, 4 new tokens, bf16, 33.9 us = 4.5 TB/s; 256
 // entries of up to 8, fp32, 260 us = 4.6 TB/s; folds of up to 8 tokens, bf16,
-// 58.3 us = 4.7 TB/s; 128 entries of up to 17, fp32, 220 us = 5.0 TB/s.  (A copy
-// reaches 4.75 TB/s.)  A wave's own time is latency: its vector instructions
+// 60 us = 4.6 TB/s, 4 us of it the launch that advances the rings; 128 entries of
+// up to 17, fp32, 221 us = 5.0 TB/s.  (A copy reaches 4.75 TB/s.)  A wave's own time is latency: its vector instructions
 // are busy for a quarter of it, its matrix instructions for a tenth.
 //
 // Step.  With M = P T (P_ij = scale e^(G_i - G_j) q^_i . k^_j) the outputs need
