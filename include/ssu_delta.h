@@ -12,9 +12,11 @@
  *   S <- exp(g_t) S;  u_t = b_t (v_t - S k^_t);  S <- S + u_t k^_t^T
  *   o_t = scale S q^_t
  * Everything between the inputs and the outputs is computed in fp32 (decay
- * sums in fp64); matrix products take operands that are not bf16 in two or
- * three bf16 parts: fp32 states and fp32 outputs end about 1e-6 of their norm
- * or less from the exact ones.
+ * sums in fp64); operands of matrix products that are not bf16 enter them in
+ * three bf16 parts (24 bits) or, where the result is rounded to 16 bits anyway,
+ * in two.  On ordinary inputs fp32 outputs, and the final states that a prompt
+ * gives beside them, end 1e-7 to 2e-7 of their norm from the exact ones; the
+ * final states beside bf16 outputs end within about 1e-6.
  * Infinities or NaN in a token's inputs may reach every output of the call for
  * its request and head (the tokens before it in the call too), and nothing
  * else.

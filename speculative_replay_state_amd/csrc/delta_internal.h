@@ -16,13 +16,13 @@ constexpr float kDeltaEps = 1e-6f;     // under the root of the unit length of q
 constexpr int kDeltaMaxDv = 256;
 constexpr int kChunk = 32;             // tokens of a prompt chunk: one K = 32 MFMA step over tokens
 
-// Scratch of one (chunk, value head): T - I, T = (I + A)^-1, in two bf16 parts,
-// the chunk's factors, and P in two parts (towards bf16 outputs) or three
-// (fp32); both triangles as MFMA row operands without their zero upper blocks.
+// Scratch of one (chunk, value head): T - I, T = (I + A)^-1, the chunk's factors,
+// and P, both triangles as MFMA row operands without their zero upper blocks, in
+// two bf16 parts towards bf16 outputs and in three towards fp32 ones.
 constexpr int kRecPart = 64 * (8 + 16);  // rows 0..15: 8 bytes a lane; rows 16..31: 16 bytes
-constexpr int kRecT = 2 * kRecPart;
 constexpr int kRecF = 544;  // f32: b[32], b e^G rk[32], e^(Gw-G) rk[32], scale rq e^G[32], e^Gw
-constexpr int rec_bytes(int parts) { return kRecT + kRecF + parts * kRecPart; }
+constexpr int rec_t(int parts) { return parts * kRecPart; }
+constexpr int rec_bytes(int parts) { return rec_t(parts) + kRecF + parts * kRecPart; }
 constexpr int kRecMax = rec_bytes(3);
 
 struct DCache {

@@ -9,13 +9,15 @@
 // by delta_scan_kernel (a wave per 16 columns of dim_v) where there are many
 // such chains, by delta_chain_kernel (six waves per 16 columns) where there
 // are few and each chunk's latency adds up.  Products with q, k and v take them
-// as they are (bf16); the state enters the products with k and q in two bf16
-// parts, R the one with T - I in two (T - I too; the identity's share of U is
-// R in fp32), U the update in three and, with P, the outputs in two, or three
-// where they are fp32.  Against 64 bits, fp32 states end 3e-7 to 8e-7 of their
-// norm off, fp32 outputs 7e-7 to 1.1e-6 (with two parts 4e-6, for 691 us where
-// three take 742); with T R in fp32 products the states 1e-7 to 2e-7, and the
-// calls below 622 and 511 us.
+// as they are (bf16).  Of what else enters a product, the update keeps 24 bits
+// (three bf16 parts); the state, T - I, R (the identity's share of U is R in
+// fp32), P and U keep as many towards fp32 outputs and 16 (two parts) towards
+// bf16 ones, whose own rounding is 500 times what that loses.  Against 64 bits,
+// of their norm: fp32 outputs end 1.3e-7 to 1.7e-7 off and the states beside them
+// 1.3e-7 to 1.5e-7 (fp32 torch products 2e-7 and 1e-7); the states beside bf16
+// outputs 2e-7 to 6e-7.  With S, T - I and R in two parts towards fp32 outputs as
+// well these end 1.0e-6 off, in 665 us instead of 795 for the 8 sequences below,
+// in 515 instead of 568 for the one; with P and U in two too, 4e-6.
 //
 // What bounds them, at 8 sequences of 2048 to 4096 tokens with 64 heads of dim
 // 128, 600 us: the chunk kernel takes 118 us (0.32 GB of records written), the
@@ -59,7 +61,7 @@ __device__ __forceinline__ bool seq_rows(const DPrefill &p, int s, int &b0, int 
   return b0 >= 0 && b0 <= b1 && b1 <= p.rows;
 }
 
-// Parts of P and U in their product.
+// Parts of what is not bf16 and enters a product.
 constexpr int out_parts(int OT) { return OT == kOutF32 ? 3 : 2; }
 
 // Rows 16 ti .. of a 32 x 32 lower triangle as row operands of NP bf16 parts,
@@ -82,6 +84,10 @@ __device__ __forceinline__ u32x2 short_row(const uint8_t *at, int a, int lane) {
 template <int NP>
 __device__ __forceinline__ bf16x8 long_row(const uint8_t *at, int a, int lane) {
   return __builtin_bit_cast(bf16x8, ld16(at + NP * 64 * 8 + (a * 64 + lane) * 16));
+}
+__device__ __forceinline__ u32x2 lower(bf16x8 f) {
+  const u32x4 w = __builtin_bit_cast(u32x4, f);
+  return u32x2{w[0], w[1]};
 }
 __device__ __forceinline__ bf16x8 halves(u32x2 a, u32x2 b) { return __builtin_bit_cast(bf16x8, u32x4{a[0], a[1], b[0], b[1]}); }
 
@@ -171,7 +177,7 @@ __global__ __launch_bounds__(64, 3) void delta_chunk_kernel(DPrefill p, int per,
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           x[4 * a + e] = a <= ti && 16 * a + 4 * q + e <= i ? r * decay[a <= ti ? ti + a : 0][e] * qk[a <= ti ? ti + a : 0][e] : 0.f;
-      write_rows<NP>(rec + kRecT + kRecF, ti, lane, x);
+      write_rows<NP>(rec + rec_t(NP) + kRecF, ti, lane, x);
     }
     wave_sync();
     invert_diag<kChunk>(w, lane);
@@ -181,9 +187,9 @@ __global__ __launch_bounds__(64, 3) void delta_chunk_kernel(DPrefill p, int per,
       t_row<kChunk>(w, ti, m, q, x);
 #pragma unroll
       for (int e = 0; e < 4; ++e) x[4 * ti + e] = 4 * q + e == m ? 0.f : x[4 * ti + e];  // T - I
-      write_rows<2>(rec, ti, lane, x);
+      write_rows<NP>(rec, ti, lane, x);
     }
-    float *f = reinterpret_cast<float *>(rec + kRecT);
+    float *f = reinterpret_cast<float *>(rec + rec_t(NP));
     if (lane < kChunk) {
       const double Gw = w.G[kChunk - 1];
       const float e = exp2_d(G), rk = w.rk[lane];
@@ -200,11 +206,12 @@ __global__ __launch_bounds__(64, 3) void delta_chunk_kernel(DPrefill p, int per,
 // the state the rows n = n0 + 32 i + 8 q + 4 a + r in S[i][a][r], of the tokens
 // the rows 16 ti + 4 q + r.
 
-// S in 16 of its 24 bits enters the products with k and q, which moves a state
-// by 2^-20.6 of its norm in the mean (two bf16 parts, each rounded to nearest).
-__device__ __forceinline__ void split_state(const f32x4 (&S)[2], bf16x8 (&f)[2]) {
+// S enters the products with k and q in NP parts, each rounded to nearest: two
+// move a state by 2^-20.6 of its norm in the mean.
+template <int NP>
+__device__ __forceinline__ void split_state(const f32x4 (&S)[2], bf16x8 (&f)[NP]) {
   const float y[8] = {S[0][0], S[0][1], S[0][2], S[0][3], S[1][0], S[1][1], S[1][2], S[1][3]};
-  split<2>(y, f);
+  split<NP>(y, f);
 }
 // 16 tokens of k or q along n0 .. n0 + 31
 template <int DK>
@@ -213,9 +220,10 @@ __device__ __forceinline__ bf16x8 row_tile(const uint16_t *rows, int n0, int ti,
 }
 
 // What a chunk's residuals and update take from LDS beside k.
+template <int NP>
 struct Factors {
-  u32x2 ts[2];  // T's rows in two parts
-  bf16x8 tl[2];
+  u32x2 ts[NP];  // T - I, its rows in parts
+  bf16x8 tl[NP];
   f32x4 b[2], be[2], e[2];  // b, b e^G / |k|, e^(G_w - G) / |k| of the lane's tokens
   s16x4 v[2];
   float ew;
@@ -224,9 +232,9 @@ struct Factors {
     const int m = lane & 15, q = lane >> 4;
     const float *fac = in.factors();
 #pragma unroll
-    for (int a = 0; a < 2; ++a) {
+    for (int a = 0; a < NP; ++a) {
       ts[a] = short_row(in.rec, a, lane);
-      tl[a] = long_row<2>(in.rec, a, lane);
+      tl[a] = long_row<NP>(in.rec, a, lane);
     }
 #pragma unroll
     for (int ti = 0; ti < 2; ++ti) {
@@ -243,22 +251,30 @@ struct Factors {
     ew = fac[128];
   }
   // U = R + (T - I) R with R = b V - (b e^G / |k|) K S^T: the identity's part in
-  // fp32, the other from T - I and R in two parts each.  (The first 16 tokens have
+  // fp32, the other from T - I and R in NP parts each.  (The first 16 tokens have
   // only themselves before them: two products of parts fill a depth of 32.)
   __device__ __forceinline__ void residuals(const f32x4 (&x)[2], f32x4 (&U)[2]) const {
     float R[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       R[i] = fmaf(-be[i / 4][i % 4], x[i / 4][i % 4], b[i / 4][i % 4] * bf2f((uint16_t)v[i / 4][i % 4]));
-    bf16x8 f[2];
-    split<2>(R, f);
-    const u32x4 r0 = __builtin_bit_cast(u32x4, f[0]), r1 = __builtin_bit_cast(u32x4, f[1]);
-    const bf16x8 ts01 = halves(ts[0], ts[1]);
-    U[0] = mfma_bf16(ts01, halves(u32x2{r1[0], r1[1]}, u32x2{r1[0], r1[1]}), f32x4{R[0], R[1], R[2], R[3]});
-    U[1] = mfma_bf16(tl[1], f[0], f32x4{R[4], R[5], R[6], R[7]});
-    U[0] = mfma_bf16(ts01, halves(u32x2{r0[0], r0[1]}, u32x2{r0[0], r0[1]}), U[0]);
-    U[1] = mfma_bf16(tl[0], f[1], U[1]);
-    U[1] = mfma_bf16(tl[0], f[0], U[1]);
+    bf16x8 f[NP];
+    split<NP>(R, f);
+    u32x2 r[NP];
+#pragma unroll
+    for (int a = 0; a < NP; ++a) r[a] = lower(f[a]);
+    U[0] = f32x4{R[0], R[1], R[2], R[3]};
+    U[1] = f32x4{R[4], R[5], R[6], R[7]};
+    if constexpr (NP == 3) {
+      U[0] = mfma_bf16(halves(ts[2], ts[1]), halves(r[0], r[1]), U[0]);
+      U[0] = mfma_bf16(halves(ts[0], ts[1]), halves(r[2], r[0]), U[0]);
+      U[0] = mfma_bf16(halves(ts[0], ts[0]), halves(r[1], r[0]), U[0]);
+    } else {
+      const bf16x8 both = halves(ts[0], ts[1]);
+      U[0] = mfma_bf16(both, halves(r[1], r[1]), U[0]);
+      U[0] = mfma_bf16(both, halves(r[0], r[0]), U[0]);
+    }
+    U[1] = mfma_parts(tl, f, U[1]);
   }
   // e^(G_w - G) U / |k| in 24 bits
   __device__ __forceinline__ void update(const f32x4 (&U)[2], bf16x8 (&f)[3]) const {
@@ -291,7 +307,7 @@ __device__ __forceinline__ void write_outputs(const DPrefill &p, const Chain &n,
   const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(static_cast<uint8_t *>(p.out) + (int64_t)row0 * row_bytes, 0,
                                                       rows * row_bytes, 0x00020000);
   constexpr int NP = out_parts(OT);
-  const uint8_t *P = in.rec + kRecT + kRecF;
+  const uint8_t *P = in.rec + rec_t(NP) + kRecF;
   bf16x8 f[NP];
 #pragma unroll
   for (int a = 0; a < NP; ++a) f[a] = ti == 0 ? halves(short_row(P, a, lane), u32x2{0, 0}) : long_row<NP>(P, a, lane);
@@ -392,8 +408,8 @@ inline dim3 chain_grid(const DPrefill &p, int groups, int unit) {
 // two workgroups share a CU (8 sequences of 2048 to 4096 tokens, 64 heads of
 // dim 128: 800 us with one and three buffers, 691 with two).  The bf16 form fits
 // the 128 registers of that by itself; the fp32 form of whole heads is held to
-// them, which spills a few (742 us for 3000 tokens each; 771 with 166 registers
-// and one workgroup).
+// them, which spills two (795 us; 880 with 169 registers and one workgroup, 865
+// with half a head in each).
 template <int OT, int DK, int NC>
 __global__ __launch_bounds__(NC * 64, OT == kOutF32 ? NC / 2 : 2) void delta_scan_kernel(DPrefill p, int groups, int unit) {
   constexpr int COLS = NC * 16, NK = DK / 32, NP = out_parts(OT);
@@ -423,24 +439,25 @@ __global__ __launch_bounds__(NC * 64, OT == kOutF32 ? NC / 2 : 2) void delta_sca
       // x = K S^T (rows = tokens), o = Q S^T (transposed: columns = tokens)
 #pragma unroll
       for (int i = 0; i < NK; ++i) {
-        bf16x8 fs[2], kf[2], qf[2];
-        split_state(S[i], fs);
+        bf16x8 fs[NP], kf[2], qf[2];
+        split_state<NP>(S[i], fs);
 #pragma unroll
         for (int ti = 0; ti < 2; ++ti) {
           kf[ti] = row_tile<DK>(in.k, 32 * i, ti, lane);
           qf[ti] = row_tile<DK>(in.q, 32 * i, ti, lane);
         }
 #pragma unroll
-        for (int a = 1; a >= 0; --a)
+        for (int a = NP - 1; a >= 0; --a)
 #pragma unroll
           for (int ti = 0; ti < 2; ++ti) {
             x[ti] = mfma_bf16(kf[ti], fs[a], x[ti]);
             o[ti] = mfma_bf16(fs[a], qf[ti], o[ti]);
           }
       }
-      Factors fac;
+      Factors<NP> fac;
       fac.load_residual(in, wave, lane);
       fac.residuals(x, U);
+      if constexpr (OT == kOutF32) __builtin_amdgcn_sched_barrier(0);  // (the update's factors read earlier would spill)
       // S <- e^(G_w) S + (e^(G_w - G) U / |k|)^T K
       fac.load_update(in, lane);
       bf16x8 fw[3], fu[NP];
@@ -469,8 +486,8 @@ __global__ __launch_bounds__(NC * 64, OT == kOutF32 ? NC / 2 : 2) void delta_sca
 // helpers write chunk c + 2 and read c - 1 meanwhile: four buffers.
 template <int OT, int DK>
 __global__ __launch_bounds__(6 * 64, 1) void delta_chain_kernel(DPrefill p, int groups, int unit) {
-  constexpr int NS = 2, NH = 4, NK = DK / 32 / NS;
-  typedef Chunk<DK, 16, out_parts(OT)> Buf;
+  constexpr int NS = 2, NH = 4, NK = DK / 32 / NS, NP = out_parts(OT);
+  typedef Chunk<DK, 16, NP> Buf;
   __shared__ Buf buf[4];
   __shared__ f32x4 red_x[2][NS][2][64], red_o[2][NS][2][64], shared_u[2][2][64];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, m = lane & 15, q = lane >> 4;
@@ -488,7 +505,7 @@ __global__ __launch_bounds__(6 * 64, 1) void delta_chain_kernel(DPrefill p, int 
       __syncthreads();
       struct Held {
         bf16x8 k[NK][2], q[NK][2], kt[NK][2];
-        Factors fac;
+        Factors<NP> fac;
       };
       auto hold = [&](int c, Held &h) {
         const Buf &in = buf[c & 3];
@@ -504,15 +521,15 @@ __global__ __launch_bounds__(6 * 64, 1) void delta_chain_kernel(DPrefill p, int 
         h.fac.load_update(in, lane);
       };
       auto step = [&](int c, const Held &has, Held &next) {
-        bf16x8 fs[NK][2];
+        bf16x8 fs[NK][NP];
         f32x4 x[2], o[2], U[2], other[2];
         x[0] = x[1] = o[0] = o[1] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int i = 0; i < NK; ++i) split_state(S[i], fs[i]);
+        for (int i = 0; i < NK; ++i) split_state<NP>(S[i], fs[i]);
 #pragma unroll
         for (int i = 0; i < NK; ++i)
 #pragma unroll
-          for (int a = 1; a >= 0; --a)
+          for (int a = NP - 1; a >= 0; --a)
 #pragma unroll
             for (int ti = 0; ti < 2; ++ti) x[ti] = mfma_bf16(has.k[i][ti], fs[i][a], x[ti]);
 #pragma unroll
@@ -525,7 +542,7 @@ __global__ __launch_bounds__(6 * 64, 1) void delta_chain_kernel(DPrefill p, int 
 #pragma unroll
         for (int i = 0; i < NK; ++i)
 #pragma unroll
-          for (int a = 1; a >= 0; --a)
+          for (int a = NP - 1; a >= 0; --a)
 #pragma unroll
             for (int ti = 0; ti < 2; ++ti) o[ti] = mfma_bf16(fs[i][a], has.q[i][ti], o[ti]);
 #pragma unroll
@@ -561,8 +578,8 @@ __global__ __launch_bounds__(6 * 64, 1) void delta_chain_kernel(DPrefill p, int 
 #pragma unroll
       for (int w = 1; w < NS; ++w) o += red_o[c & 1][w][hw & 1][lane];
       const f32x4 U[2] = {shared_u[c & 1][0][lane], shared_u[c & 1][1][lane]};
-      bf16x8 fu[out_parts(OT)];
-      split_u<out_parts(OT)>(U, fu);
+      bf16x8 fu[NP];
+      split_u<NP>(U, fu);
       write_outputs<OT>(p, n, buf[c & 3], c, hw & 1, n.c0, hw < 2, lane, fu, o);
     };
     // chunk c + SETS is fetched while c + 1 is stored: as many register sets, so

@@ -22,7 +22,7 @@ struct Chunk {
   static constexpr int KS = DK + 8, VS = COLS + 8;  // row strides: 16 rows start in different banks
   __align__(16) uint16_t k[kChunk * KS], q[kChunk * KS], v[kChunk * VS];
   __align__(16) uint8_t rec[kRec];
-  __device__ __forceinline__ const float *factors() const { return reinterpret_cast<const float *>(rec + kRecT); }
+  __device__ __forceinline__ const float *factors() const { return reinterpret_cast<const float *>(rec + rec_t(NP)); }
 };
 
 // One sequence's chunks of a head's columns c0 .. c0 + COLS - 1.
