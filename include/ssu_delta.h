@@ -14,9 +14,10 @@
  * Everything between the inputs and the outputs is computed in fp32 (decay
  * sums in fp64); operands of matrix products that are not bf16 enter them in
  * three bf16 parts (24 bits) or, where the result is rounded to 16 bits anyway,
- * in two.  On ordinary inputs fp32 outputs, and the final states that a prompt
- * gives beside them, end 1e-7 to 2e-7 of their norm from the exact ones; the
- * final states beside bf16 outputs end within about 1e-6.
+ * in two.  On ordinary inputs fp32 outputs, the final states that a prompt
+ * gives beside them and fp32 checkpoints after a fold end 1e-7 to 3e-7 of their
+ * norm from the exact ones; a prompt's final states beside bf16 outputs end
+ * within about 1e-6.
  * Infinities or NaN in a token's inputs may reach every output of the call for
  * its request and head (the tokens before it in the call too), and nothing
  * else.

@@ -5,7 +5,7 @@
 // entries of 64 heads of 128 x 128, 4 new tokens, bf16, 33.9 us = 4.5 TB/s; 256
 // entries of up to 8, fp32, 260 us = 4.6 TB/s; folds of up to 8 tokens, bf16,
 // 60 us = 4.6 TB/s, 4 us of it the launch that advances the rings; 128 entries of
-// up to 17, fp32, 221 us = 5.0 TB/s.  (A copy reaches 4.75 TB/s.)  A wave's own time is latency: its vector instructions
+// up to 17, fp32, 225 us = 4.9 TB/s.  (A copy reaches 4.75 TB/s.)  A wave's own time is latency: its vector instructions
 // are busy for a quarter of it, its matrix instructions for a tenth.
 //
 // Step.  With M = P T (P_ij = scale e^(G_i - G_j) q^_i . k^_j) the outputs need
@@ -417,7 +417,7 @@ __device__ __forceinline__ bool delta_fold_entry(const DCache &c, int slot, int 
 template <int ST, int KW, int DK>
 __global__ __launch_bounds__(64, 2) void delta_flush_kernel(DCache c, const int32_t *slot_idx, const int32_t *num_fold,
                                                             int parts, int share, int nwaves) {
-  constexpr int E = KW / 4, NT = KW / 16, NW = ST == kF32 ? 3 : 2, NS = ST == kBF16 ? 1 : 2;
+  constexpr int E = KW / 4, NT = KW / 16, NW = ST == kF32 ? 3 : 2, NS = ST == kBF16 ? 1 : NW;
   typedef typename Tok<KW>::V TV;
   typedef Rows<ST, DK> Tiles;
   typedef Window<KW, DK> Win;
@@ -482,11 +482,13 @@ __global__ __launch_bounds__(64, 2) void delta_flush_kernel(DCache c, const int3
   wave_sync();
   invert_diag<KW>(w, lane);
 
-  // T b (towards V) and W = T b e^G K^ as operands, rows = tokens.  W and an
-  // fp32 checkpoint's values enter their product in two parts (the residuals
-  // it goes into are what the fold adds, not the checkpoint itself).
+  // T b (towards V) and W = T b e^G K^ as operands, rows = tokens, in NW parts, as
+  // the update: 24 bits towards an fp32 checkpoint, with its values in as many (W
+  // and those in 16 left folds of 1 to 32 tokens with little decay 4e-7 to 1.1e-6
+  // of the state's norm off, these 7e-8 to 2.6e-7; 222 us instead of 225 for 128
+  // entries), 16 towards one whose own rounding is 2^-9 or 2^-12.
   TV ft[NT][NW];
-  bf16x8 fw[NT][DK / 32][2];
+  bf16x8 fw[NT][DK / 32][NW];
   float bj[E], ej[E];
 #pragma unroll
   for (int a = 0; a < NT; ++a)
@@ -517,7 +519,7 @@ __global__ __launch_bounds__(64, 2) void delta_flush_kernel(DCache c, const int3
 #pragma unroll
         for (int r = 0; r < 4; ++r) z[4 * a + r] = acc[r];
       }
-      split<2>(z, fw[ti][ks]);
+      split<NW>(z, fw[ti][ks]);
     }
   }
   const double Gw = w.G[KW - 1];

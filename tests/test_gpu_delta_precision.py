@@ -74,3 +74,54 @@ def test_prompt(n, tokens, hk, hv, dk, dv, init, out_name):
         if out_name == "f32":
             near(out[at].transpose(0, 1), want.transpose(0, 1), "outputs of sequence %d" % s)
         near(h1[s], S, "state of sequence %d" % s, LIMIT if out_name == "f32" else LIMIT + 2.0 ** -18)
+
+
+def cache_of(g, L, dk, dv, hv=4):
+    """fp32 checkpoints of two slots, full rings, hardly any decay."""
+    c = R.Cache(g, 3, 2, hv, dk, dv, L, "f32")
+    gates = c.t["gate_cache"].view(3, hv, L, 2)
+    gates[..., 0] = -0.02 * torch.rand(3, hv, L, generator=g)
+    gates[..., 1] = 0.5 + 0.5 * torch.rand(3, hv, L, generator=g)
+    return c
+
+
+@pytest.mark.parametrize("L,fold,dk,dv", [(16, 1, 128, 128), (16, 4, 128, 64), (16, 16, 128, 128), (32, 32, 128, 128),
+                                          (32, 20, 64, 64), (5, 5, 64, 128)])
+def test_flush(L, fold, dk, dv):
+    """The state, and what the fold leaves of it along the keys that it took out: there an operand's lost bits are not
+    averaged over the whole state."""
+    g = gen(L + fold + dk)
+    c = cache_of(g, L, dk, dv)
+    d, dc = c.upload(ssu, DEV)
+    ids = torch.tensor([2, 1], dtype=torch.int32, device=DEV)
+    ssu.delta_flush(dc, ids, torch.full_like(ids, fold))
+    back = torch.empty(2, c.hv, dv, dk, device=DEV)
+    ssu.delta_read_state(dc, back, ids)
+    for j, slot in enumerate((2, 1)):
+        k, v, gr, br = c.ring(slot, 0, fold)
+        S, _ = R.run(c.states(slot), None, k, v, gr, br, 1.0)
+        near(back[j], S, "state of slot %d" % slot)
+        keys = R.unit(k).repeat_interleave(c.hv // c.hk, 1).permute(1, 2, 0)  # [hv, dk, fold]
+        was = (c.states(slot).double() @ keys).flatten(1).norm(dim=1) + v.double().norm(dim=(0, 2))
+        off = ((back[j].cpu().double() - S) @ keys).flatten(1).norm(dim=1) / was
+        print("along the keys: %.2g to %.2g" % (off.min(), off.max()), flush=True)
+        assert bool((off <= LIMIT).all()), "along the keys off by %.3g, %.3g allowed" % (off.max(), LIMIT)
+
+
+@pytest.mark.parametrize("L,live,T,dk,dv", [(16, 0, 1, 128, 128), (16, 12, 4, 128, 64), (32, 16, 16, 128, 128), (32, 20, 7, 64, 64)])
+def test_step(L, live, T, dk, dv):
+    g = gen(L + live + dk)
+    c = cache_of(g, L, dk, dv)
+    d, dc = c.upload(ssu, DEV)
+    x = R.inputs(g, 2 * T, 2, 4, dk, dv)
+    dev = {n: t.to(DEV) for n, t in x.items()}
+    ids, out = torch.tensor([2, 1], dtype=torch.int32, device=DEV), torch.empty(2 * T, 4, dv, device=DEV)
+    ssu.delta_replay_step(dc, ssu.make_delta_step(dc, T, ids, torch.full_like(ids, live), None, dev["q"], dev["k"], dev["v"], dev["dt"],
+                                                  dev["beta"], dev["A"], dev["dt_bias"], out))
+    gates = R.gates(x["dt"], x["beta"], x["A"], x["dt_bias"])
+    for j, slot in enumerate((2, 1)):
+        at = slice(j * T, (j + 1) * T)
+        k, v, gr, br = c.ring(slot, 0, live)
+        S, _ = R.run(c.states(slot), None, k, v, gr, br, 1.0)
+        _, want = R.run(S, x["q"][at], x["k"][at], x["v"][at], gates[0][at], gates[1][at], dk ** -0.5)
+        near(out[at].transpose(0, 1), want.transpose(0, 1), "outputs of slot %d" % slot)
