@@ -17,7 +17,8 @@
  * in two.  On ordinary inputs fp32 outputs, the final states that a prompt
  * gives beside them and fp32 checkpoints after a fold end 1e-7 to 3e-7 of their
  * norm from the exact ones; a prompt's final states beside bf16 outputs end
- * within about 1e-6.
+ * 2e-7 to 1e-6 from them, up to 4e-6 where hardly anything decays (ask for fp32
+ * outputs where they have to be nearer).
  * Infinities or NaN in a token's inputs may reach every output of the call for
  * its request and head (the tokens before it in the call too), and nothing
  * else.

@@ -486,7 +486,7 @@ __global__ __launch_bounds__(64, 2) void delta_flush_kernel(DCache c, const int3
   // the update: 24 bits towards an fp32 checkpoint, with its values in as many (W
   // and those in 16 left folds of 1 to 32 tokens with little decay 4e-7 to 1.1e-6
   // of the state's norm off, these 7e-8 to 2.6e-7; 222 us instead of 225 for 128
-  // entries), 16 towards one whose own rounding is 2^-9 or 2^-12.
+  // entries), 16 towards one that rounds them to 8 or 11 bits.
   TV ft[NT][NW];
   bf16x8 fw[NT][DK / 32][NW];
   float bj[E], ej[E];

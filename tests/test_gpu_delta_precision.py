@@ -57,9 +57,12 @@ def near(got, want, what, limit=LIMIT):
     (10, 200, 2, 4, 128, 128, False), (20, 200, 2, 4, 64, 64, True),     # more of them
     (33, 100, 2, 8, 128, 128, True), (33, 100, 2, 8, 64, 128, False)])   # whole heads
 @pytest.mark.parametrize("out_name", ["f32", "bf16"])
-def test_prompt(n, tokens, hk, hv, dk, dv, init, out_name):
+@pytest.mark.parametrize("kept", [False, True])  # hardly any decay: an error stays
+def test_prompt(n, tokens, hk, hv, dk, dv, init, out_name, kept):
     g = gen(n + dk)
     x = R.inputs(g, n * tokens, hk, hv, dk, dv)
+    if kept:
+        x["A"], x["beta"] = 0.01 * x["A"], x["beta"] + 2
     h0 = 0.3 * torch.randn(n, hv, dv, dk, generator=g) if init else torch.zeros(n, hv, dv, dk)
     d = {k: v.to(DEV) for k, v in x.items()}
     out, h1 = torch.empty(n * tokens, hv, dv, dtype=R.TYPES[out_name], device=DEV), torch.empty(n, hv, dv, dk, device=DEV)
