@@ -3,8 +3,10 @@
 // Two kernels.  verify_sum_kernel, a wave per (entry, piece of 1024 values of
 // the vocabulary): the number n of accepted drafts (one lane per draft, a
 // ballot), then the sum of the residual r of row n over the piece, in fp64.
-// verify_pick_kernel, a wave per entry: the piece in which the running sum
-// passes u' sum r, the first value in it that does, and the bookkeeping.
+// verify_pick_kernel, by the first wave of a workgroup per entry: the piece in which
+// the running sum passes u' sum r, the first value in it that does, and the
+// bookkeeping.  (The other waves stand by for a residual that is empty, where the
+// row itself is summed.)
 // verify_row_kernel does both for an entry in one workgroup, where rows are
 // short or the entries many.
 //
@@ -16,7 +18,9 @@
 // us.  With four pieces a wave of
 // verify_sum_kernel 36.7, 14.9 and 10.5 us, with one 32.4, 13.1 and 8.9 (fewer
 // waves wait for their drafts); with the verdicts in a kernel of their own
-// 31.6, 15.2, 11.9.
+// 31.6, 15.2, 11.9.  An entry whose residual is empty, alone with 131072 fp32
+// values: 21 us (94 summed again by one wave); one of the 64 above, with draft
+// probabilities, 28 instead of 16 (92); one of the 256 37 instead of 27 (128).
 #include "ssu_device.cuh"
 #include "verify_internal.h"
 
@@ -148,7 +152,14 @@ __device__ __forceinline__ double piece_sum(const KVerify &v, const Verdict &o, 
   return wave_sum(sum);
 }
 
+template <int PT>
+__device__ __forceinline__ double whole_or_part(const KVerify &v, const Verdict &o, bool rejected, int piece, int lane) {
+  return (piece + 1) * kVerifyPiece <= v.vocab ? piece_sum<PT, true>(v, o, rejected, piece, lane)
+                                               : piece_sum<PT, false>(v, o, rejected, piece, lane);
+}
+
 constexpr int kSumWaves = 4;                     // waves of a workgroup of verify_sum_kernel
+constexpr int kPickWaves = 8;                    // of verify_pick_kernel
 constexpr int kRowWaves = 16, kRowPieces = 256;  // of verify_row_kernel; the pieces its LDS holds
 
 // The verdict of an entry in its words of the scratch.
@@ -176,8 +187,7 @@ __global__ __launch_bounds__(kSumWaves * 64) void verify_sum_kernel(KVerify v, i
   if (piece == 0 && lane == 0) write_verdict(o, ws, pieces);
   if (o.T <= 0) return;
   const bool rejected = o.n < o.T - 1 && o.draft >= 0;
-  const double sum = (piece + 1) * kVerifyPiece <= v.vocab ? piece_sum<PT, true>(v, o, rejected, piece, lane)
-                                                                     : piece_sum<PT, false>(v, o, rejected, piece, lane);
+  const double sum = whole_or_part<PT>(v, o, rejected, piece, lane);
   if (lane == 0) ws[piece] = sum;
 }
 
@@ -194,39 +204,41 @@ __device__ __forceinline__ double wave_scan(double x, int lane) {
 __device__ __forceinline__ int first_lane(uint64_t set) { return (int)__builtin_ctzll(set); }
 __device__ __forceinline__ int last_lane(uint64_t set) { return 63 - (int)__builtin_clzll(set); }
 
-// One wave's pick for entry b from the pieces' sums: in LDS, or in memory, where
-// it reads past its CU's own cache what it may have written itself.
+// The running sums over an entry's pieces, in LDS or in memory (where they are read
+// past the CU's own cache, since the workgroup may have written them itself).
+template <bool LDS>
+struct Sums {
+  double *at;
+  int pieces, lane;
+  double x, upto, total;  // of this lane's run of neighbouring pieces, up to its end, of all
+  __device__ __forceinline__ int first() const { return lane * ((pieces + 63) / 64); }
+  __device__ __forceinline__ int end() const { return min(first() + (pieces + 63) / 64, pieces); }
+  __device__ __forceinline__ double get(int k) const {
+    return LDS ? at[k] : __hip_atomic_load(at + k, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  __device__ __forceinline__ void set(int k, double y) const {
+    if (lane != 0) return;
+    if (LDS)
+      at[k] = y;
+    else
+      __hip_atomic_store(at + k, y, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  __device__ __forceinline__ void add_up() {
+    x = 0.0;
+    for (int k = first(); k < end(); ++k) x += get(k);
+    upto = wave_scan(x, lane);
+    total = __shfl(upto, 63);
+  }
+};
+
+// One wave's pick for entry b; `rejected` is false where an empty residual gave way
+// to the row itself.
 template <int PT, bool LDS>
-__device__ __forceinline__ void pick(const KVerify &v, const Verdict &o, double *sums, int pieces, int b, int lane) {
-  auto kept_sum = [&](int k) { return LDS ? sums[k] : __hip_atomic_load(sums + k, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); };
+__device__ __forceinline__ void pick(const KVerify &v, const Verdict &o, const Sums<LDS> &s, bool rejected, int b, int lane) {
+  const double x = s.x, upto = s.upto, total = s.total;
+  const int p0 = s.first(), p1 = s.end();
   int bits = o.bits, token = -1;
   if (o.T > 0) {
-    bool rejected = o.n < o.T - 1 && o.draft >= 0;
-    // each lane a run of neighbouring pieces
-    const int per = (pieces + 63) / 64, p0 = lane * per, p1 = min(p0 + per, pieces);
-    double x = 0.0;
-    for (int k = p0; k < p1; ++k) x += kept_sum(k);
-    double upto = wave_scan(x, lane), total = __shfl(upto, 63);
-    if (!(total > 0.0) && rejected) {  // an empty residual: the row itself
-      rejected = false;
-      for (int k = 0; k < pieces; ++k) {
-        const double y = piece_sum<PT, false>(v, o, false, k, lane);
-        if (lane == 0) {
-          if (LDS)
-            sums[k] = y;
-          else
-            __hip_atomic_store(sums + k, y, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        }
-      }
-      if (LDS)
-        wave_sync();
-      else
-        __threadfence();
-      x = 0.0;
-      for (int k = p0; k < p1; ++k) x += kept_sum(k);
-      upto = wave_scan(x, lane);
-      total = __shfl(upto, 63);
-    }
     if (!(total > 0.0) || total > 1.7e308) {
       bits |= SSU_STATUS_BAD_PROBS;
     } else {
@@ -239,7 +251,7 @@ __device__ __forceinline__ void pick(const KVerify &v, const Verdict &o, double 
       int piece = -1;
       double before = upto - x, at = 0.0;  // (in lane `run`)
       for (int k = p0; k < p1; ++k) {
-        const double y = kept_sum(k);
+        const double y = s.get(k);
         if (y > 0.0) {
           piece = k;
           at = before;
@@ -315,11 +327,25 @@ __device__ __forceinline__ void pick(const KVerify &v, const Verdict &o, double 
   }
 }
 
+// Where the residual is empty the row itself is summed, by all waves; each sees for
+// itself whether it is wanted (the same sums, so the same in all).
 template <int PT>
-__global__ __launch_bounds__(64) void verify_pick_kernel(KVerify v, int pieces) {
-  const int b = blockIdx.x;
+__global__ __launch_bounds__(kPickWaves * 64) void verify_pick_kernel(KVerify v, int pieces) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, b = blockIdx.x;
   double *ws = v.ws + (int64_t)b * (pieces + 2);
-  pick<PT, false>(v, read_verdict(v, ws, pieces, b), ws, pieces, b, threadIdx.x);
+  const Verdict o = read_verdict(v, ws, pieces, b);
+  bool rejected = o.n < o.T - 1 && o.draft >= 0;
+  Sums<false> s = {ws, pieces, lane, 0.0, 0.0, 0.0};
+  if (rejected || (wave == 0 && o.T > 0)) s.add_up();
+  if (rejected && !(s.total > 0.0)) {
+    rejected = false;
+    __syncthreads();  // (every wave has read the sums)
+    for (int k = wave; k < pieces; k += kPickWaves) s.set(k, whole_or_part<PT>(v, o, false, k, lane));
+    __threadfence();
+    __syncthreads();
+    if (wave == 0) s.add_up();
+  }
+  if (wave == 0) pick<PT, false>(v, o, s, rejected, b, lane);
 }
 
 // Both at once: a workgroup per entry, its sums in LDS; every wave forms the
@@ -327,18 +353,27 @@ __global__ __launch_bounds__(64) void verify_pick_kernel(KVerify v, int pieces) 
 template <int PT>
 __global__ __launch_bounds__(kRowWaves * 64) void verify_row_kernel(KVerify v, int pieces) {
   __shared__ double sums[kRowPieces];
+  __shared__ int some[kRowWaves];  // whether a wave has found mass
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, b = blockIdx.x;
   const Verdict o = verdict<PT>(v, b, lane);
-  if (o.T > 0) {
-    const bool rejected = o.n < o.T - 1 && o.draft >= 0;
+  bool rejected = o.n < o.T - 1 && o.draft >= 0;
+  Sums<true> s = {sums, pieces, lane, 0.0, 0.0, 0.0};
+  while (o.T > 0) {
+    bool mass = false;
     for (int k = wave; k < pieces; k += kRowWaves) {
-      const double sum = (k + 1) * kVerifyPiece <= v.vocab ? piece_sum<PT, true>(v, o, rejected, k, lane)
-                                                                     : piece_sum<PT, false>(v, o, rejected, k, lane);
-      if (lane == 0) sums[k] = sum;
+      const double y = whole_or_part<PT>(v, o, rejected, k, lane);
+      mass |= y > 0.0;
+      s.set(k, y);
     }
+    if (lane == 0) some[wave] = mass;
+    __syncthreads();
+    if (!rejected || __ballot(some[lane % kRowWaves]) != 0) break;
+    rejected = false;  // an empty residual: the row itself
+    __syncthreads();   // (every wave has looked)
   }
-  __syncthreads();
-  if (wave == 0) pick<PT, true>(v, o, sums, pieces, b, lane);
+  if (wave != 0) return;
+  if (o.T > 0) s.add_up();
+  pick<PT, true>(v, o, s, rejected, b, lane);
 }
 
 template <int PT>
@@ -358,7 +393,7 @@ hipError_t verify_pt(const KVerify &v, hipStream_t st) {
   verify_sum_kernel<PT><<<grid, dim3(kSumWaves * 64), 0, st>>>(v, pieces);
   const hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;
-  verify_pick_kernel<PT><<<dim3((unsigned)v.batch), dim3(64), 0, st>>>(v, pieces);
+  verify_pick_kernel<PT><<<dim3((unsigned)v.batch), dim3(kPickWaves * 64), 0, st>>>(v, pieces);
   return hipGetLastError();
 }
 
