@@ -19,8 +19,8 @@
 // verify_sum_kernel 36.7, 14.9 and 10.5 us, with one 32.4, 13.1 and 8.9 (fewer
 // waves wait for their drafts); with the verdicts in a kernel of their own
 // 31.6, 15.2, 11.9.  An entry whose residual is empty, alone with 131072 fp32
-// values: 21 us (94 summed again by one wave); one of the 64 above, with draft
-// probabilities, 28 instead of 16 (92); one of the 256 37 instead of 27 (128).
+// values: 23 us (94 summed again by one wave); one of the 64 above, with draft
+// probabilities, 27 instead of 16 (92); one of the 256 36 instead of 26 (128).
 #include "ssu_device.cuh"
 #include "verify_internal.h"
 
@@ -327,23 +327,28 @@ __device__ __forceinline__ void pick(const KVerify &v, const Verdict &o, const S
   }
 }
 
-// Where the residual is empty the row itself is summed, by all waves; each sees for
-// itself whether it is wanted (the same sums, so the same in all).
+// Where the residual is empty the row itself is summed, by all waves (they wait for
+// the first one's word: with each adding up the sums for itself a row of 2^24 values
+// took 133 us, of which 23 were theirs).
 template <int PT>
 __global__ __launch_bounds__(kPickWaves * 64) void verify_pick_kernel(KVerify v, int pieces) {
+  __shared__ int empty;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, b = blockIdx.x;
   double *ws = v.ws + (int64_t)b * (pieces + 2);
   const Verdict o = read_verdict(v, ws, pieces, b);
-  bool rejected = o.n < o.T - 1 && o.draft >= 0;
+  bool rejected = o.n < o.T - 1 && o.draft >= 0;  // (the same in every wave)
   Sums<false> s = {ws, pieces, lane, 0.0, 0.0, 0.0};
-  if (rejected || (wave == 0 && o.T > 0)) s.add_up();
-  if (rejected && !(s.total > 0.0)) {
-    rejected = false;
-    __syncthreads();  // (every wave has read the sums)
-    for (int k = wave; k < pieces; k += kPickWaves) s.set(k, whole_or_part<PT>(v, o, false, k, lane));
-    __threadfence();
+  if (wave == 0 && o.T > 0) s.add_up();
+  if (rejected) {
+    if (threadIdx.x == 0) empty = !(s.total > 0.0);
     __syncthreads();
-    if (wave == 0) s.add_up();
+    if (empty) {
+      rejected = false;
+      for (int k = wave; k < pieces; k += kPickWaves) s.set(k, whole_or_part<PT>(v, o, false, k, lane));
+      __threadfence();
+      __syncthreads();
+      if (wave == 0) s.add_up();
+    }
   }
   if (wave == 0) pick<PT, false>(v, o, s, rejected, b, lane);
 }
