@@ -272,12 +272,15 @@ struct Factors {
       U[0] = mfma_bf16(halves(ts[2], ts[1]), halves(r[0], r[1]), U[0]);
       U[0] = mfma_bf16(halves(ts[0], ts[1]), halves(r[2], r[0]), U[0]);
       U[0] = mfma_bf16(halves(ts[0], ts[0]), halves(r[1], r[0]), U[0]);
-    } else {
+      U[1] = mfma_parts(tl, f, U[1]);
+    } else {  // the two sums in turn: one after the other 64 chains of 2048 tokens take 136 us instead of 131
       const bf16x8 both = halves(ts[0], ts[1]);
       U[0] = mfma_bf16(both, halves(r[1], r[1]), U[0]);
+      U[1] = mfma_bf16(tl[1], f[0], U[1]);
       U[0] = mfma_bf16(both, halves(r[0], r[0]), U[0]);
+      U[1] = mfma_bf16(tl[0], f[1], U[1]);
+      U[1] = mfma_bf16(tl[0], f[0], U[1]);
     }
-    U[1] = mfma_parts(tl, f, U[1]);
   }
   // e^(G_w - G) U / |k| in 24 bits
   __device__ __forceinline__ void update(const f32x4 (&U)[2], bf16x8 (&f)[3]) const {
