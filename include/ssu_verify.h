@@ -58,7 +58,7 @@ enum {
  *   workspace   at least ssu_verify_workspace_size(batch, vocab) bytes,
  *               16-byte aligned; calls that may overlap need one each.
  * Requirements: 1 <= max_seqlen <= 64, 1 <= vocab <= 2^24, batch <= 65535,
- * batch * ceil(vocab / 4096) <= 2^23, the probabilities aligned to their type
+ * batch * ceil(vocab / 4096) <= 2^23 (workgroups of a launch), the probabilities aligned to their type
  * (rows a multiple of 16 bytes apart are read a little faster), the rest
  * 4-byte.  The rows that cu_seqlens names are rows of the
  * tensors (the call does not know how many there are); a length outside [0,

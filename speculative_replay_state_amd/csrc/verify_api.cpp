@@ -18,8 +18,9 @@ int check_sizes(int32_t batch, int32_t vocab) {
   if (batch > 65535) return api_fail(SSU_ERR_UNSUPPORTED, "batch %d exceeds 65535 entries per call", batch);
   if (vocab < 1) return api_fail(SSU_ERR_INVALID, "vocab must be positive (got %d)", vocab);
   if (vocab > (1 << 24)) return api_fail(SSU_ERR_UNSUPPORTED, "vocab %d exceeds 2^24", vocab);
-  if ((int64_t)batch * ((vocab + 4095) / 4096) > (1 << 23))
-    return api_fail(SSU_ERR_UNSUPPORTED, "batch %d x vocab %d exceeds 2^23 pieces of 4096 values per call", batch, vocab);
+  if ((int64_t)batch * ((vocab + ssu::kVerifyGroup - 1) / ssu::kVerifyGroup) > (1 << 23))  // a grid's threads fit 32 bits
+    return api_fail(SSU_ERR_UNSUPPORTED, "batch %d x vocab %d exceeds 2^23 workgroups of %d values per call", batch, vocab,
+                    ssu::kVerifyGroup);
   return SSU_OK;
 }
 

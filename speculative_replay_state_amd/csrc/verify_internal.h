@@ -13,6 +13,7 @@ namespace ssu {
 enum ProbType { kPF32 = 0, kPBF16 = 1, kPF16 = 2 };
 
 constexpr int kVerifyPiece = 1024;    // values of a row whose sum is kept: 16 a lane
+constexpr int kVerifyGroup = 4096;    // of a row in one workgroup of the sums, a piece a wave
 constexpr int kVerifyMaxTokens = 64;  // the drafts of an entry are tested by the lanes of one wave
 
 inline int verify_pieces(int vocab) { return (vocab + kVerifyPiece - 1) / kVerifyPiece; }

@@ -158,9 +158,9 @@ __device__ __forceinline__ double whole_or_part(const KVerify &v, const Verdict 
                                                : piece_sum<PT, false>(v, o, rejected, piece, lane);
 }
 
-constexpr int kSumWaves = 4;                     // waves of a workgroup of verify_sum_kernel
-constexpr int kPickWaves = 8;                    // of verify_pick_kernel
-constexpr int kRowWaves = 16, kRowPieces = 256;  // of verify_row_kernel; the pieces its LDS holds
+constexpr int kSumWaves = kVerifyGroup / kVerifyPiece;  // waves of a workgroup of verify_sum_kernel
+constexpr int kPickWaves = 8;                           // of verify_pick_kernel
+constexpr int kRowWaves = 16, kRowPieces = 256;         // of verify_row_kernel; the pieces its LDS holds
 
 // The verdict of an entry in its words of the scratch.
 __device__ __forceinline__ Verdict read_verdict(const KVerify &v, const double *ws, int pieces, int b) {
