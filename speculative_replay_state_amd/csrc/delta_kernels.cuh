@@ -4,9 +4,12 @@
 // Both are bound by HBM, the checkpoint read once (and written once): 64
 // entries of 64 heads of 128 x 128, 4 new tokens, bf16, 33.9 us = 4.5 TB/s; 256
 // entries of up to 8, fp32, 260 us = 4.6 TB/s; folds of up to 8 tokens, bf16,
-// 60 us = 4.6 TB/s, 4 us of it the launch that advances the rings; 128 entries of
-// up to 17, fp32, 225 us = 4.9 TB/s.  (A copy reaches 4.75 TB/s.)  A wave's own time is latency: its vector instructions
-// are busy for a quarter of it, its matrix instructions for a tenth.
+// 59 us = 4.6 TB/s, 4 us of it the launch that advances the rings; 128 entries of
+// up to 17, fp32, 225 us = 4.9 TB/s.  (A copy reaches 4.75 TB/s.)  A wave's own
+// time is latency: its vector instructions are busy for a quarter of it, its
+// matrix instructions for a tenth.  64 entries of 4 tokens with 16 live in a ring
+// of 32, bf16: 37 us; one entry 8.1 (6.7 with a ring of 16).  Init and read of 64
+// entries, bf16: 84 and 80 us, 5.0 and 5.1 TB/s; of one, 11.
 //
 // Step.  With M = P T (P_ij = scale e^(G_i - G_j) q^_i . k^_j) the outputs need
 // neither U nor the state's products with k:

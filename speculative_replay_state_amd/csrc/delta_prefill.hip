@@ -23,12 +23,13 @@
 // us instead of 586 and in 538 instead of 473.
 //
 // What bounds them, at 8 sequences of 2048 to 4096 tokens with 64 heads of dim
-// 128, 600 us: the chunk kernel takes 118 us (0.32 GB of records written), the
-// scan 480; its matrix instructions are busy for two fifths of that and its
-// other vector instructions for as long, which four waves a SIMD hardly
-// overlap.  One sequence of 16384 tokens, 32 heads, 468 us: 50 us of chunks,
+// 128, 577 to 630 us with the card's clock: the chunk kernel takes 120 us (0.32 GB
+// of records written), the scan 470 to 540; LDS is busy for 59 % of that, matrix
+// instructions for 44, other vector instructions for 46, which four waves a SIMD
+// hardly overlap.  One sequence of 16384 tokens, 32 heads, 471 us: 50 us of chunks,
 // then 0.82 us for each of 512, a chain of 150 vector instructions, three
-// products and one exchange through LDS.
+// products and one exchange through LDS.  16 sequences of 351 to 701 tokens, 32
+// heads of dim 64, 74 us: 29 and 45, the latency of 22 chunks in a row.
 #include <algorithm>
 
 #include "delta_device.cuh"

@@ -12,9 +12,9 @@
 //
 // What bounds them is one read of row n of both distributions, behind the
 // drafts' own (dependent) reads.  256 entries of 8 tokens, 131072 bf16 values in
-// two distributions: 27.1 us, 4.9 TB/s (32.1 in two launches); 64 entries,
+// two distributions: 26.5 us, 5.0 TB/s (32.1 in two launches); 64 entries,
 // 100003 fp32 values without draft probabilities (rows no 16 bytes apart):
-// 12.7 us (13.5 with those rows read 4 bytes a lane); one entry of 32000: 7.8
+// 13.0 us (13.5 with those rows read 4 bytes a lane); one entry of 32000: 7.9
 // us.  With four pieces a wave of
 // verify_sum_kernel 36.7, 14.9 and 10.5 us, with one 32.4, 13.1 and 8.9 (fewer
 // waves wait for their drafts); with the verdicts in a kernel of their own

@@ -3,7 +3,9 @@ chunks, replayed steps, flushes) beside the selective state update.
 
 Argument marshalling only, as in the package's front end.  A cache or a call
 description is checked once, when it is made; it keeps its tensors alive, and
-their contents (slots, counts, inputs) may change between calls.
+their contents (slots, counts, inputs) may change between calls.  Tensors given
+to a call itself (slot_idx, num_fold, states) are not kept: on a `stream` that
+is not torch's current one they have to live until the call has run there.
 """
 from __future__ import annotations
 
