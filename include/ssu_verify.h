@@ -58,11 +58,12 @@ enum {
  *   workspace   at least ssu_verify_workspace_size(batch, vocab) bytes,
  *               16-byte aligned; calls that may overlap need one each.
  * Requirements: 1 <= max_seqlen <= 64, 1 <= vocab <= 2^24, batch <= 65535,
- * batch * ceil(vocab / 4096) <= 2^23 (workgroups of a launch), the probabilities aligned to their type
- * (rows a multiple of 16 bytes apart are read a little faster), the rest
- * 4-byte.  The rows that cu_seqlens names are rows of the
- * tensors (the call does not know how many there are); a length outside [0,
- * max_seqlen] counts as none, with SSU_STATUS_BAD_SEQLEN.  Outputs must not
+ * batch * ceil(vocab / 4096) <= 2^23 (workgroups of a launch), the
+ * probabilities aligned to their type (rows a multiple of 16 bytes apart are
+ * read a little faster), the rest 4-byte.  The rows that cu_seqlens names are
+ * rows of the tensors (the call does not know how many there are); a length
+ * outside [0, max_seqlen] counts as none, with SSU_STATUS_BAD_SEQLEN.  An entry
+ * whose residual is empty has its row read once more.  Outputs must not
  * overlap inputs except as said above.  batch == 0 is a no-op.
  */
 typedef struct ssu_verify_args {

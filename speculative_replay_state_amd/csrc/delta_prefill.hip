@@ -12,15 +12,15 @@
 // as they are (bf16).  Of what else enters a product, the update keeps 24 bits
 // (three bf16 parts); the state, T - I, R (the identity's share of U is R in
 // fp32), P and U keep as many towards fp32 outputs and 16 (two parts) towards
-// bf16 ones, whose own rounding is hundreds of times what that loses.  Against 64 bits,
-// of their norm: fp32 outputs end 1.3e-7 to 1.7e-7 off and the states beside them
-// 1.3e-7 to 1.5e-7, 2.6e-7 where hardly anything decays (fp32 torch products 2e-7
-// and 1e-7, 3e-7); the states beside bf16 outputs 2e-7 to 9e-7, 3e-6.  With S, T - I
-// and R in two parts towards fp32 outputs as well these end 1.0e-6 off, in 665 us
-// instead of 795 for the 8 sequences below, in 515 instead of 568 for the one;
-// with P and U in two too, 4e-6.  With S, T - I and R in three towards bf16
-// outputs as well the states beside them are like those beside fp32 ones, in 705
-// us instead of 586 and in 538 instead of 473.
+// bf16 ones, whose own rounding is hundreds of times what that loses.  Off from 64
+// bits, of their norm: fp32 outputs 1.3e-7 to 1.8e-7 and the states beside them 8e-8
+// to 1.5e-7, either 2.6e-7 where hardly anything decays (fp32 torch products 2e-7 and
+// 1e-7, 3e-7); the states beside bf16 outputs 2e-7 to 9e-7, 3e-6.
+// With S, T - I and R in two parts towards fp32 outputs too these end 1.0e-6 off,
+// in 665 us instead of 795 for the 8 sequences below, in 515 instead of 568 for
+// the one; with P and U in two as well, 4e-6.  With S, T - I and R in three towards
+// bf16 outputs too the states there are as near as beside fp32 ones, in 705 us
+// instead of 586 and in 538 instead of 473.
 //
 // What bounds them, at 8 sequences of 2048 to 4096 tokens with 64 heads of dim
 // 128, 577 to 630 us with the card's clock: the chunk kernel takes 120 us (0.32 GB
