@@ -6,11 +6,14 @@ tensors and calls the library.  Every step of the computation runs in the
 library's HIP kernels.  Importing fails loudly when libssu.so has not been
 built (python speculative_replay_state_amd/build.py); there is no fallback.
 
-The gated delta rule (include/ssu_delta.h) and the verification of drafted
-tokens (include/ssu_verify.h) are bound in delta.py and verification.py; their
-front ends (DeltaCache, make_delta_step, delta_replay_step, delta_flush,
-make_delta_prefill, delta_prefill, make_verify, verify, ...) are names of
-this package too.
+The gated delta rule (include/ssu_delta.h), the verification of drafted tokens
+(include/ssu_verify.h), prompts and checkpoints read back (include/ssu_prefill.h)
+and token histories and logits (include/ssu_logits.h) are bound in delta.py,
+verification.py, prompts.py and sampling.py; their front ends (DeltaCache,
+make_delta_step, delta_replay_step, delta_flush, make_delta_prefill,
+delta_prefill, make_verify, verify, make_prefill, prefill, read_state,
+TokenHistory, make_count, count, make_logits, logits, ...) are names of this
+package too.
 
 Names follow the C ABI: ssu_init_state, ssu_replay_step, ssu_flush,
 ssu_workspace_size, ssu_resolve_algo, ssu_last_error, plus DeviceCache (the
@@ -356,3 +359,8 @@ from .delta import (  # noqa: E402
     delta_prefill, delta_prefill_workspace_size, delta_read_state, delta_replay_step, make_delta_prefill, make_delta_step)
 from .verification import (  # noqa: E402
     SSU_STATUS_BAD_PROBS, SSU_STATUS_BAD_TOKEN, SsuVerify, make_verify, verify, verify_workspace_size)
+# prompts and checkpoints read back; token histories and logits
+from .prompts import SsuPrefill, make_prefill, prefill, prefill_workspace_size, read_state  # noqa: E402
+from .sampling import (  # noqa: E402
+    SSU_STATUS_BAD_BIAS, SSU_STATUS_EMPTY_ROW, SsuCount, SsuHistory, SsuLogits, TokenHistory, count, logits,
+    logits_workspace_size, make_count, make_logits)

@@ -6,7 +6,8 @@
 
 Compiles the device code in parallel (csrc/ssu_kernels.cuh and
 csrc/delta_kernels.cuh through their *_inst.hip, once per state type;
-delta_prefill.hip; verify_kernels.hip), the dispatch (csrc/ssu_launch.cpp)
+delta_prefill.hip; prefill.hip; read_kernels.hip; verify_kernels.hip;
+logits_kernels.hip), the dispatch (csrc/ssu_launch.cpp)
 and the host entry points (csrc/*_api.cpp), and links them into
 speculative_replay_state_amd/libssu.so.
 """
@@ -64,8 +65,8 @@ def build(verbose: bool = False) -> str:
             objs.append(o)
             jobs.append([hipcc, "--offload-arch=" + ARCH, *COMMON, "-DSSU_INST_ST=%d" % st, "-c",
                          os.path.join(CSRC, "delta_kernels_inst.hip"), "-o", o])
-        for src in ("delta_prefill.hip", "verify_kernels.hip", "ssu_launch.cpp", "ssu_api.cpp", "delta_api.cpp",
-                    "verify_api.cpp"):
+        for src in ("delta_prefill.hip", "prefill.hip", "read_kernels.hip", "verify_kernels.hip", "logits_kernels.hip",
+                    "ssu_launch.cpp", "ssu_api.cpp", "delta_api.cpp", "prefill_api.cpp", "verify_api.cpp", "logits_api.cpp"):
             o = os.path.join(tmp, os.path.splitext(src)[0] + ".o")
             objs.append(o)
             jobs.append([hipcc, "--offload-arch=" + ARCH, *COMMON, "-x", "hip", "-c", os.path.join(CSRC, src),

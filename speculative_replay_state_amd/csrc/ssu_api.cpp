@@ -9,8 +9,8 @@
 
 #include <hip/hip_runtime.h>
 
-#include "../../include/ssu.h"
-#include "ssu_internal.h"
+#include "../../include/ssu_prefill.h"
+#include "prefill_internal.h"
 
 namespace ssu {
 
@@ -217,6 +217,7 @@ int check_step(const ssu_cache *c, const ssu_step *s) {
 constexpr size_t kNoAllocBytes = SSU_NOALLOC_SCRATCH_BYTES;
 static __device__ __align__(256) unsigned char scratch[kNoAllocBytes];
 
+constexpr int64_t kReadMaxPairs = (int64_t)1 << 21;
 constexpr int kMaxDevices = 64;
 std::mutex g_scratch_mu;
 void *g_scratch_dev[kMaxDevices] = {};
@@ -397,6 +398,28 @@ int ssu_init_state(const ssu_cache *cache, const float *states, int64_t states_b
     return fail(SSU_ERR_INVALID, "states must be 16-byte aligned with a stride that is a multiple of 4");
   hipError_t err = ssu::launch_init(kcache(cache, sr_seed), states, states_batch_stride, slot_idx, n,
                                     state_type_of(raw(cache->state_dtype)), stream);
+  if (err != hipSuccess) return fail(SSU_ERR_HIP, "kernel launch failed: %s", hipGetErrorString(err));
+  return ok();
+}
+
+int ssu_read_state(const ssu_cache *cache, float *states, int64_t states_batch_stride, const int32_t *slot_idx, int32_t n,
+                   int32_t recur, hipStream_t stream) {
+  int rc = check_cache(cache);
+  if (rc != SSU_OK) return rc;
+  if (n < 0) return fail(SSU_ERR_INVALID, "n must be >= 0 (got %d)", n);
+  if (n == 0) return ok();
+  if ((int64_t)n * cache->nheads > kReadMaxPairs)
+    return fail(SSU_ERR_UNSUPPORTED, "n %d x nheads %d exceeds 2^21 (entry, head) pairs per call", n, cache->nheads);
+  if (recur && !cache->recur_state) return fail(SSU_ERR_INVALID, "the cache has no recur_state to read");
+  if (!states || !slot_idx) return fail(SSU_ERR_INVALID, "states and slot_idx must not be NULL");
+  const int64_t packed = (int64_t)cache->nheads * ssu::kHeadDim * ssu::kDState;
+  if (states_batch_stride < packed || states_batch_stride % 4 != 0)
+    return fail(SSU_ERR_INVALID, "states_batch_stride %lld must be a multiple of 4 and at least one packed state (%lld)",
+                (long long)states_batch_stride, (long long)packed);
+  if (!aligned16(states) || !aligned4(slot_idx))
+    return fail(SSU_ERR_INVALID, "states must be 16-byte aligned, slot_idx 4-byte");
+  hipError_t err = ssu::launch_read(kcache(cache, 0), states, states_batch_stride, slot_idx, n,
+                                    state_type_of(raw(cache->state_dtype)), recur ? 1 : 0, stream);
   if (err != hipSuccess) return fail(SSU_ERR_HIP, "kernel launch failed: %s", hipGetErrorString(err));
   return ok();
 }
