@@ -45,7 +45,7 @@ int check_sizes(int64_t rows, int64_t n, int64_t heads) {
 size_t state_bytes(int64_t slots, int64_t heads) { return (size_t)(slots * heads * ssu::kHeadDim * ssu::kDState) * sizeof(float); }
 size_t bytes_for(int64_t rows, int64_t n, int64_t heads) {
   const int64_t seg = ssu::prefill_segment(rows, n, heads);
-  if (rows <= seg) return 0;
+  if (rows <= 2 * seg) return 0;
   const int64_t slots = ssu::prefill_slots(rows, n, seg);
   return state_bytes(slots, heads) + (size_t)(slots * heads) * sizeof(double);
 }
