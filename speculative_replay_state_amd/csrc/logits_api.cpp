@@ -194,6 +194,9 @@ int ssu_logits(const ssu_history *history, const ssu_logits_args *a, hipStream_t
   l.mask_stride = a->mask_row_stride;
   l.ws = static_cast<float2 *>(a->workspace);
   l.status = a->status;
+  // What is more than the last cache's 256 MiB would only push itself out of it (bf16 rows of 131072 values, 512 of them
+  // 88 -> 76 us, 1024 185 -> 159; f32 ones 187 -> 153; 256 bf16 rows 45.7 -> 46.1), and less is there for who reads it next.
+  l.past = (int64_t)a->rows * a->vocab * (isz + osz) >= (int64_t)256 << 20;
   return launched(ssu::launch_logits(khistory(history), l, it, ot, !a->no_softmax, stream));
 }
 

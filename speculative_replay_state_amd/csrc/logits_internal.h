@@ -45,6 +45,7 @@ struct KLogits {
   const uint32_t *mask;
   int64_t mask_stride;  // words between rows
   float2 *ws;           // [batch * T][pieces]
+  bool past;            // the outputs are stored past the caches
   int32_t *status;
 };
 

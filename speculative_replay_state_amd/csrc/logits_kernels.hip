@@ -1,10 +1,18 @@
 // Token histories (ssu_history_count) and logits (ssu_logits).
 //
-// A row's values go through registers 8 neighbours a lane.  Few of them are
-// special, in the history, among the drafts or biased: a workgroup marks those of its
-// range in a bitmap in LDS, numbers them by the set bits before them, and a thread
-// each forms their x (a load of the logit and of the count, all at once) into LDS,
-// from where the lane that holds the value takes it.
+// The softmax takes every value twice, for the largest x and the sum of exp((x - m) /
+// temperature), and for the probabilities; memory bounds it from some hundred rows on
+// (each value in and out once: a row stays in the caches between the two).  The values
+// go through registers 8 neighbours a lane, with a byte of a bitmap in LDS that says
+// which of them are not taken as they are: these become NaN, which counts for nothing
+// (a maximum passes over it, the exponential's own bounds of 0 and 1 make it 0; so a
+// value costs some ten instructions in each of the two).  Those in the history, among
+// the drafts or biased are special: a workgroup lists the special tokens of its range, a
+// thread each forms their x (the loads of the logit and of the count on their way at
+// once), and each is added to the sums and written by itself, behind the rest.  With a
+// copy of the row in registers and a third of the waves in its place 1536 rows of 131072
+// bf16 values took 329 us for 276 now, 205 of them without history, biases and masks;
+// 162 is what the bytes take at a copy's 5.1 TB/s.
 #include "logits_internal.h"
 #include "ssu_device.cuh"
 
@@ -20,15 +28,8 @@ namespace {
 // histories
 // ---------------------------------------------------------------------------
 
-// A workgroup per entry.  A word of `counts` whose bit was not set yet is
-// emptied by the one thread that sets the bit, then all tokens are added:
-// nothing but the bits has to be cleared for a new request.
-template <int NT>
-__global__ __launch_bounds__(NT) void count_kernel(KHistory h, KCount c) {
-  const int b = blockIdx.x, tid = threadIdx.x, slot = c.slot_idx[b];
-  if (slot <= 0 || slot >= h.num_slots) return;
-  int64_t first = (int64_t)b * c.T;
-  int n = c.T;
+// Tokens [first, first + n) of entry b; false (and said so) where they are not what they have to be.
+__device__ __forceinline__ bool count_range(const KHistory &h, const KCount &c, int b, int tid, int64_t &first, int &n) {
   bool ok;
   if (c.cu) {
     const int b0 = c.cu[b], b1 = c.cu[b + 1];
@@ -36,13 +37,24 @@ __global__ __launch_bounds__(NT) void count_kernel(KHistory h, KCount c) {
     first = b0;
     n = b1 - b0;
   } else {
-    if (c.num) n = c.num[b];
+    first = (int64_t)b * c.T;
+    n = c.num ? c.num[b] : c.T;
     ok = n >= 0 && n <= c.T;
   }
-  if (!ok) {
-    if (tid == 0 && h.status) atomicOr(h.status, SSU_STATUS_BAD_SEQLEN);
-    return;
-  }
+  if (!ok && tid == 0 && h.status) atomicOr(h.status, SSU_STATUS_BAD_SEQLEN);
+  return ok;
+}
+
+// A workgroup per entry.  A word of `counts` whose bit was not set yet is
+// emptied by the one thread that sets the bit, then all tokens are added:
+// nothing but the bits has to be cleared for a new request.
+template <int NT>
+__global__ __launch_bounds__(NT) void count_kernel(KHistory h, KCount c) {
+  const int b = blockIdx.x, tid = threadIdx.x, slot = c.slot_idx[b];
+  if (slot <= 0 || slot >= h.num_slots) return;
+  int64_t first;
+  int n;
+  if (!count_range(h, c, b, tid, first, n)) return;
   uint32_t *seen = h.seen + (int64_t)slot * h.seen_stride;
   int32_t *counts = h.counts + (int64_t)slot * h.counts_stride;
   const int32_t *tokens = c.tokens + first;
@@ -82,6 +94,44 @@ __global__ __launch_bounds__(NT) void count_kernel(KHistory h, KCount c) {
   }
 }
 
+// A prompt's tokens, each counted once: a workgroup per entry collects their bits in
+// LDS, as many words as there are, and adds them to the page without an atomic (a
+// text's frequent tokens share a few words: with one for each token 32 prompts of 2048 to
+// 4096 took 46 us).
+constexpr int kPromptWords = 4096;
+template <int NT>
+__global__ __launch_bounds__(NT) void count_prompt_kernel(KHistory h, KCount c) {
+  __shared__ uint32_t mine[kPromptWords];
+  const int b = blockIdx.x, tid = threadIdx.x, slot = c.slot_idx[b];
+  if (slot <= 0 || slot >= h.num_slots) return;
+  int64_t first;
+  int n;
+  if (!count_range(h, c, b, tid, first, n)) return;
+  for (int w = tid; w < h.words; w += NT) mine[w] = 0;
+  __syncthreads();
+  const int32_t *tokens = c.tokens + first;
+  bool bad = false;
+  for (int i = tid; i < n; i += NT) {
+    const int tok = tokens[i];
+    const bool in = tok >= 0 && tok < h.vocab;
+    bad |= !in;
+    if (in) atomicOr(&mine[tok >> 5], 1u << (tok & 31));
+  }
+  if (bad && h.status) atomicOr(h.status, SSU_STATUS_BAD_TOKEN);
+  __syncthreads();
+  uint32_t *seen = h.seen + (int64_t)slot * h.seen_stride;
+  int32_t *counts = h.counts + (int64_t)slot * h.counts_stride;
+  for (int w = tid; w < h.words; w += NT) {
+    const uint32_t add = mine[w], old = c.reset ? 0u : seen[w];
+    if (c.reset || (add & ~old)) seen[w] = old | add;
+    for (uint32_t v = add; v; v &= v - 1) {
+      const int k = __builtin_ctz(v);
+      int32_t *at = counts + 32 * w + k;
+      *at = (old >> k) & 1u ? *at | 1 : 1;
+    }
+  }
+}
+
 // ---------------------------------------------------------------------------
 // logits
 // ---------------------------------------------------------------------------
@@ -107,57 +157,49 @@ struct Eight {
     const uint16_t h = (uint16_t)(w[0][k / 2] >> (16 * (k & 1)));
     return IT == kLBF16 ? bf2f(h) : (float)__builtin_bit_cast(_Float16, h);
   }
-  // values i .. i + 7 of a row of n; past its end the last one, again
-  __device__ __forceinline__ void load(const uint8_t *row, int i, int n) {
-    constexpr int S = logit_size(IT);
-    if (i + 8 <= n) {
-      const uint8_t *at = row + (int64_t)i * S;
-      w[0] = *reinterpret_cast<const u32x4_any *>(at);
-      if constexpr (IT == kLF32) w[1] = *reinterpret_cast<const u32x4_any *>(at + 16);
-      return;
-    }
+  // (what was unpacked of them is not worth its registers until they are wanted again)
+  __device__ __forceinline__ void again() {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const int at = min(i + k, n - 1);
-      if constexpr (IT == kLF32) {
-        w[k / 4][k % 4] = reinterpret_cast<const uint32_t *>(row)[at];
-      } else {
-        const uint32_t v = reinterpret_cast<const uint16_t *>(row)[at];
-        w[0][k / 2] = k & 1 ? (w[0][k / 2] & 0xFFFFu) | (v << 16) : v;
-      }
-    }
+    for (u32x4 &v : w) asm volatile("" : "+v"(v));
+  }
+  __device__ __forceinline__ void load(const uint8_t *row, int i) {
+    const uint8_t *at = row + (int64_t)i * logit_size(IT);
+    w[0] = *reinterpret_cast<const u32x4_any *>(at);
+    if constexpr (IT == kLF32) w[1] = *reinterpret_cast<const u32x4_any *>(at + 16);
   }
 };
 
 template <int OT>
-__device__ __forceinline__ void store8(uint8_t *row, int i, int n, const float (&v)[8]) {
+__device__ __forceinline__ void store1(uint8_t *row, int i, float v) {
+  if constexpr (OT == kLF32)
+    reinterpret_cast<float *>(row)[i] = v;
+  else
+    reinterpret_cast<uint16_t *>(row)[i] = (uint16_t)(OT == kLBF16 ? pack_bf16(v, 0.f) : pack_f16(v, 0.f));
+}
+__device__ __forceinline__ void store16(uint8_t *at, u32x4 v, bool past) {
+  if (past)
+    __builtin_nontemporal_store(v, reinterpret_cast<u32x4_any *>(at));
+  else
+    *reinterpret_cast<u32x4_any *>(at) = v;
+}
+// past: by the caches
+template <int OT>
+__device__ __forceinline__ void store8(uint8_t *row, int i, const float (&v)[8], bool past) {
   uint8_t *at = row + (int64_t)i * logit_size(OT);
-  if (i + 8 <= n) {
-    if constexpr (OT == kLF32) {
-      u32x4 a, b;
+  u32x4 a;
+  if constexpr (OT == kLF32) {
+    u32x4 b;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        a[k] = __float_as_uint(v[k]);
-        b[k] = __float_as_uint(v[4 + k]);
-      }
-      *reinterpret_cast<u32x4_any *>(at) = a;
-      *reinterpret_cast<u32x4_any *>(at + 16) = b;
-    } else {
-      u32x4 a;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) a[k] = OT == kLBF16 ? pack_bf16(v[2 * k], v[2 * k + 1]) : pack_f16(v[2 * k], v[2 * k + 1]);
-      *reinterpret_cast<u32x4_any *>(at) = a;
+    for (int k = 0; k < 4; ++k) {
+      a[k] = __float_as_uint(v[k]);
+      b[k] = __float_as_uint(v[4 + k]);
     }
-    return;
-  }
+    store16(at + 16, b, past);
+  } else {
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    if (i + k >= n) break;
-    if constexpr (OT == kLF32)
-      reinterpret_cast<float *>(at)[k] = v[k];
-    else
-      reinterpret_cast<uint16_t *>(at)[k] = (uint16_t)(OT == kLBF16 ? pack_bf16(v[k], 0.f) : pack_f16(v[k], 0.f));
+    for (int k = 0; k < 4; ++k) a[k] = OT == kLBF16 ? pack_bf16(v[2 * k], v[2 * k + 1]) : pack_f16(v[2 * k], v[2 * k + 1]);
   }
+  store16(at, a, past);
 }
 
 // What a workgroup needs of its row.
@@ -171,7 +213,7 @@ struct Row {
   const int32_t *bias_tok;
   const float *bias_val;
   int nb;
-  const uint8_t *mask;    // NULL: all
+  const uint32_t *mask;   // NULL: all
   float rep, freq, pres, temperature;
 };
 
@@ -216,7 +258,7 @@ __device__ __forceinline__ bool find_row(const KHistory &h, const KLogits &l, in
       atomicOr(l.status, SSU_STATUS_BAD_BIAS);
     }
   }
-  r.mask = l.mask ? reinterpret_cast<const uint8_t *>(l.mask + r.row * l.mask_stride) : nullptr;
+  r.mask = l.mask ? l.mask + r.row * l.mask_stride : nullptr;
   r.rep = l.repetition ? l.repetition[b] : 1.f;
   r.freq = l.frequency ? l.frequency[b] : 0.f;
   r.pres = l.presence ? l.presence[b] : 0.f;
@@ -234,31 +276,43 @@ __device__ __forceinline__ float special_x(const Row &r, float x, bool biased, f
   return x;
 }
 
-// The special tokens of the values [i0, i0 + 32 * words) of a row.
+// The special tokens of the values [i0, i0 + 32 * words) of a row, CAP of them at a time.
 template <int NT, int WORDS, int CAP>
 struct Special {
-  uint32_t bits[WORDS];
-  uint16_t rank[WORDS];    // set bits before the word
-  uint32_t info[CAP];      // by rank: 256 (its last bias + 1) + its drafts
-  float x[CAP];            // by rank
+  uint32_t bits[WORDS];     // special
+  uint32_t out[WORDS];      // special, or left out by the mask
+  uint32_t rank[WORDS / 2]; // special ones before every other word
+  uint32_t info[CAP];       // 256 (its last bias + 1) + its drafts, later x
+  uint32_t token[CAP];      // in the range
   int sums[NT / 64];
 
-  __device__ __forceinline__ int at(int i) const {  // rank of value i of the range
-    return rank[i >> 5] + __builtin_popcount(bits[i >> 5] & ((1u << (i & 31)) - 1u));
+  __device__ __forceinline__ int at(int o) const {  // rank of the range's value o
+    const int w = o >> 5;
+    return (int)rank[w >> 1] + ((w & 1) ? __builtin_popcount(bits[w - 1]) : 0) + __builtin_popcount(bits[w] & ((1u << (o & 31)) - 1u));
   }
+  // The words of a thread, an even one first and an even number of them but for the last.
+  static __device__ __forceinline__ void share(int words, int tid, int &w0, int &w1) {
+    const int each = (words + 2 * NT - 1) / (2 * NT) * 2;
+    w0 = min(tid * each, words);
+    w1 = min(w0 + each, words);
+  }
+  __device__ __forceinline__ float x(int j) const { return __uint_as_float(info[j]); }
+  // which of values o .. o + 7 of the range are not taken as they are
+  __device__ __forceinline__ uint32_t out8(int o) const { return reinterpret_cast<const uint8_t *>(out)[o >> 3]; }
 
-  // By the whole workgroup; the number of special tokens (more than CAP: only their bits are there).
-  template <int IT>
-  __device__ __forceinline__ int build(const Row &r, int i0, int words, int vocab, int tid) {
-    if (!r.seen && r.nd == 0 && r.nb == 0) return 0;
+  // By the whole workgroup: the bitmaps; the number of special tokens.
+  __device__ __forceinline__ int mark(const Row &r, int i0, int words, int vocab, int tid) {
     const int end = min(i0 + 32 * words, vocab);
+    const bool some = r.seen || r.nd > 0 || r.nb > 0 || (vocab & 7);
     for (int w = tid; w < words; w += NT) {
-      uint32_t v = r.seen ? r.seen[(i0 >> 5) + w] : 0u;
-      const int left = vocab - i0 - 32 * w;
-      if (left < 32) v &= (1u << left) - 1u;  // (left > 0: the words are the vocabulary's)
-      bits[w] = v;
+      const int left = vocab - i0 - 32 * w;  // (> 0: the words are the vocabulary's)
+      const uint32_t real = left < 32 ? (1u << left) - 1u : ~0u;
+      // (the row's last values that are no eight go with the special ones)
+      bits[w] = (r.seen ? r.seen[(i0 >> 5) + w] & real : 0u) | (left < 32 ? real & ~((1u << (left & 24)) - 1u) : 0u);
+      out[w] = r.mask ? ~r.mask[(i0 >> 5) + w] : 0u;
     }
     __syncthreads();
+    if (!some) return 0;
     if (r.nd > 0 || r.nb > 0) {
       for (int j = tid; j < r.nd; j += NT) {
         const int k = r.drafts[j];
@@ -270,9 +324,9 @@ struct Special {
       }
       __syncthreads();
     }
-    // set bits before each word: a thread takes neighbouring words
-    const int lane = tid & 63, each = (words + NT - 1) / NT, w0 = min(tid * each, words), w1 = min(w0 + each, words);
-    int mine = 0;
+    const int lane = tid & 63;
+    int w0, w1, mine = 0;
+    share(words, tid, w0, w1);
     for (int w = w0; w < w1; ++w) mine += __builtin_popcount(bits[w]);
     int upto = mine;
 #pragma unroll
@@ -288,237 +342,384 @@ struct Special {
       if (k < (tid >> 6)) before += sums[k];
       total += sums[k];
     }
-    if (total == 0 || (CAP < 32 * WORDS && total > CAP)) return total;
     for (int w = w0; w < w1; ++w) {
-      rank[w] = (uint16_t)before;
-      for (uint32_t v = bits[w]; v; v &= v - 1) {
-        x[before] = __int_as_float(32 * w + __builtin_ctz(v));
-        info[before++] = 0;
-      }
+      if (!(w & 1)) rank[w >> 1] = (uint32_t)before;
+      before += __builtin_popcount(bits[w]);
+    }
+    return total;
+  }
+
+  // By the whole workgroup: special tokens first .. first + n - 1 with their x (-inf where the mask takes them or it is
+  // NaN), and into `out`.  (n <= CAP; all have read what was there.)
+  template <int IT>
+  __device__ __forceinline__ void form(const Row &r, int i0, int words, int vocab, int first, int n, int tid) {
+    const int end = min(i0 + 32 * words, vocab);
+    int w0, w1, j = 0;
+    share(words, tid, w0, w1);
+    if (w0 < w1) j = (int)rank[w0 >> 1] - first;
+    for (int w = w0; w < w1; ++w) {
+      for (uint32_t v = bits[w]; v; v &= v - 1, ++j)
+        if (j >= 0 && j < n) {
+          token[j] = 32 * w + __builtin_ctz(v);
+          info[j] = 0;
+        }
     }
     __syncthreads();
     if (r.nb > 0) {
       for (int j = tid; j < r.nb; j += NT) {
         const int k = r.bias_tok[j];
-        if (k >= i0 && k < end) atomicMax(&info[at(k - i0)], (uint32_t)(j + 1) << 8);
+        if (k < i0 || k >= end) continue;
+        const int p = at(k - i0) - first;
+        if (p >= 0 && p < n) atomicMax(&info[p], (uint32_t)(j + 1) << 8);
       }
       __syncthreads();
     }
     if (r.nd > 0) {
       for (int j = tid; j < r.nd; j += NT) {
         const int k = r.drafts[j];
-        if (k >= i0 && k < end) atomicAdd(&info[at(k - i0)], 1u);
+        if (k < i0 || k >= end) continue;
+        const int p = at(k - i0) - first;
+        if (p >= 0 && p < n) atomicAdd(&info[p], 1u);
       }
       __syncthreads();
     }
-    for (int j = tid; j < total; j += NT) {
-      const int i = i0 + __float_as_int(x[j]);
+    for (int j = tid; j < n; j += NT) {
+      const int o = token[j], i = i0 + o;
       const uint32_t f = info[j];
       const float v = logit_at<IT>(r.in, i);
-      int n = (int)(f & 255u);
-      bool was = n > 0;
-      if (r.seen && (r.seen[i >> 5] >> (i & 31)) & 1u) {
-        was = true;
-        n += r.counts[i] >> 1;
-      }
-      x[j] = special_x(r, v, f >> 8, f >> 8 ? r.bias_val[(f >> 8) - 1] : 0.f, was, n);
-    }
-    __syncthreads();
-    return total;
-  }
-
-  // x of the values i .. i + 7 of the row (i0 the range's start), -inf where there is none.
-  template <int IT>
-  __device__ __forceinline__ void values(const Row &r, const Eight<IT> &e, int total, int i0, int i, int vocab, float (&v)[8]) const {
-#pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = e.value(k);
-    if (total > 0) {
-      const int o = i - i0;
-      const uint32_t word = bits[o >> 5], byte = (word >> (o & 31)) & 255u;
-      if (byte) {
-        if (CAP >= 32 * WORDS || total <= CAP) {
-          int j = at(o);
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            if ((byte >> k) & 1u) v[k] = x[j++];
-        } else {
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            if ((byte >> k) & 1u) v[k] = slow(r, v[k], i + k);
+      int m = (int)(f & 255u);
+      bool was = m > 0;
+      if (r.seen) {
+        const int c = r.counts[i] >> 1;  // (loaded with the logit)
+        if ((r.seen[i >> 5] >> (i & 31)) & 1u) {
+          was = true;
+          m += c;
         }
       }
+      const bool taken = !r.mask || ((r.mask[i >> 5] >> (i & 31)) & 1u);
+      const float y = special_x(r, v, f >> 8, f >> 8 ? r.bias_val[(f >> 8) - 1] : 0.f, was, m);
+      info[j] = __float_as_uint(taken && y == y ? y : -INFINITY);
+      atomicOr(&out[o >> 5], 1u << (o & 31));
     }
-    uint32_t allowed = r.mask && i < vocab ? r.mask[i >> 3] : 255u;
-    if (i + 8 > vocab) allowed &= i < vocab ? (1u << (vocab - i)) - 1u : 0u;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = (allowed >> k) & 1u && v[k] == v[k] ? v[k] : -INFINITY;
-  }
-
-  // Where the range holds more special tokens than LDS has room for.
-  static __device__ __forceinline__ float slow(const Row &r, float x, int i) {
-    int bias = -1, n = 0;
-    for (int j = 0; j < r.nb; ++j)
-      if (r.bias_tok[j] == i) bias = j;
-    for (int j = 0; j < r.nd; ++j) n += r.drafts[j] == i;
-    bool was = n > 0;
-    if (r.seen && (r.seen[i >> 5] >> (i & 31)) & 1u) {
-      was = true;
-      n += r.counts[i] >> 1;
-    }
-    return special_x(r, x, bias >= 0, bias >= 0 ? r.bias_val[bias] : 0.f, was, n);
+    __syncthreads();
   }
 };
 
-// The largest x and sum of exp((x - m) / temperature), or for the greedy
-// choice the index of the first x = m (in the bits of s).
+// Eight values of a row, NaN where the byte has a bit: it counts for nothing below.
+template <int IT>
+__device__ __forceinline__ void values8(const Eight<IT> &e, uint32_t out, float (&v)[8]) {
+#pragma unroll
+  for (int k = 0; k < 8; ++k) v[k] = __uint_as_float(__float_as_uint(e.value(k)) | (uint32_t)((int32_t)(out << (31 - k)) >> 31));
+}
+
+// The largest x and the sum of exp((x - m) / temperature), of the finite m next to it.
 struct Stat {
   float m, s;
 };
-__device__ __forceinline__ float decay_to(float m, float M, float k) {
-  return __builtin_amdgcn_exp2f((m - fmaxf(M, -FLT_MAX)) * k);
-}
-__device__ __forceinline__ Stat join(Stat a, Stat b, float k, bool greedy) {
-  if (greedy) {
-    const bool first = a.m > b.m || (a.m == b.m && __float_as_uint(a.s) <= __float_as_uint(b.s));
-    return Stat{first ? a.m : b.m, first ? a.s : b.s};
-  }
-  Stat o;
-  o.m = fmaxf(a.m, b.m);
-  o.s = a.s * decay_to(a.m, o.m, k) + b.s * decay_to(b.m, o.m, k);
-  return o;
-}
+constexpr Stat kNoStat = {-INFINITY, 0.f};
 // log2(e) / temperature, finite and positive: (x - m) times it is 0 at x = m and -inf at x = -inf
 __device__ __forceinline__ float slope(float temperature) {
   return fminf(fmaxf(1.4426950408889634f / temperature, FLT_MIN), FLT_MAX);
 }
-__device__ __forceinline__ bool is_greedy(float temperature) { return !(temperature > 0.f); }
-
-__device__ __forceinline__ void add8(Stat &o, float (&v)[8], int i, float k, bool greedy) {
-#pragma unroll
-  for (int e = 0; e < 8; ++e) v[e] = fminf(v[e], FLT_MAX);
-  if (greedy) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (v[e] > o.m) {
-        o.m = v[e];
-        o.s = __uint_as_float((uint32_t)(i + e));
-      }
-    return;
-  }
+__device__ __forceinline__ float finite(float x) { return fminf(fmaxf(x, -FLT_MAX), FLT_MAX); }
+// exp2 between 0 and 1, 0 of NaN: of x = +inf and the largest finite m 1.  (The bounds are the instruction's own.)
+__device__ __forceinline__ float exp_of(float d) { return __builtin_amdgcn_fmed3f(__builtin_amdgcn_exp2f(d), 0.f, 1.f); }
+__device__ __forceinline__ Stat join(Stat a, Stat b, float k) {
+  const float m = fmaxf(a.m, b.m), M = finite(m);
+  return Stat{m, a.s * exp_of((a.m - M) * k) + b.s * exp_of((b.m - M) * k)};
+}
+template <int N>
+__device__ __forceinline__ void add_values(Stat &o, const float *v, float k) {
   float m = o.m;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) m = fmaxf(m, v[e]);
-  const float M = fmaxf(m, -FLT_MAX);
-  float s = o.s * __builtin_amdgcn_exp2f((o.m - M) * k);
+  for (int e = 0; e < N; ++e) m = fmaxf(m, v[e]);
+  const float M = finite(m);
+  float s = o.s * exp_of((o.m - M) * k);
 #pragma unroll
-  for (int e = 0; e < 8; ++e) s += __builtin_amdgcn_exp2f((v[e] - M) * k);
+  for (int e = 0; e < N; ++e) s += exp_of((v[e] - M) * k);
   o.m = m;
   o.s = s;
 }
-__device__ __forceinline__ Stat no_stat(bool greedy) { return Stat{-INFINITY, greedy ? __uint_as_float(~0u) : 0.f}; }
-
+__device__ __forceinline__ Stat wave_join(Stat s, float k) {
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) s = join(s, Stat{__shfl_xor(s.m, d), __shfl_xor(s.s, d)}, k);
+  return s;
+}
 // In every thread.
 template <int NT>
-__device__ __forceinline__ Stat block_join(Stat s, Stat *lds, int tid, float k, bool greedy) {
-#pragma unroll
-  for (int d = 32; d > 0; d >>= 1) s = join(s, Stat{__shfl_xor(s.m, d), __shfl_xor(s.s, d)}, k, greedy);
+__device__ __forceinline__ Stat block_join(Stat s, Stat *lds, int tid, float k) {
+  s = wave_join(s, k);
   __syncthreads();
   if ((tid & 63) == 0) lds[tid >> 6] = s;
   __syncthreads();
   Stat o = lds[0];
 #pragma unroll
-  for (int w = 1; w < NT / 64; ++w) o = join(o, lds[w], k, greedy);
+  for (int w = 1; w < NT / 64; ++w) o = join(o, lds[w], k);
   return o;
 }
 
-// The probabilities of eight values of a row whose statistics are s.
-__device__ __forceinline__ void probs8(float (&v)[8], int i, Stat s, float inv, float k, bool greedy) {
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    if (greedy)
-      v[e] = (uint32_t)(i + e) == __float_as_uint(s.s) ? 1.f : 0.f;
-    else
-      v[e] = __builtin_amdgcn_exp2f((fminf(v[e], FLT_MAX) - fmaxf(s.m, -FLT_MAX)) * k) * inv;
-  }
+// A greedy row, temperature <= 0 or NaN: the largest x (at most the largest finite) above -inf and its lowest place.
+__device__ __forceinline__ bool is_greedy(float temperature) { return !(temperature > 0.f); }
+struct Best {
+  float m;
+  int i;
+};
+constexpr Best kNoBest = {-INFINITY, 0x7fffffff};
+__device__ __forceinline__ Best better(Best a, Best b) { return b.m > a.m || (b.m == a.m && b.i < a.i) ? b : a; }
+__device__ __forceinline__ void add_best(Best &o, float x, int i) {
+  if (x > -INFINITY) o = better(o, Best{fminf(x, FLT_MAX), i});
 }
-__device__ __forceinline__ float inverse(Stat s) { return s.m > -INFINITY ? 1.f / s.s : 0.f; }
+template <int NT>
+__device__ __forceinline__ Best block_best(Best s, Best *lds, int tid) {
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) s = better(s, Best{__shfl_xor(s.m, d), __shfl_xor(s.i, d)});
+  __syncthreads();
+  if ((tid & 63) == 0) lds[tid >> 6] = s;
+  __syncthreads();
+  Best o = lds[0];
+#pragma unroll
+  for (int w = 1; w < NT / 64; ++w) o = better(o, lds[w]);
+  return o;
+}
+
+// The probabilities of a row: exp((x - m) / temperature) / sum.
+struct Probs {
+  float M, k, inv;
+  __device__ __forceinline__ Probs(Stat s, float slope) : M(finite(s.m)), k(slope), inv(s.m > -INFINITY ? 1.f / s.s : 0.f) {}
+  __device__ __forceinline__ float operator()(float x) const { return exp_of((x - M) * k) * inv; }
+};
+
+// Says so where an entry's biased tokens are none.
+__device__ __forceinline__ void bad_biases(const Row &r, const KLogits &l, int tid, int nthreads) {
+  bool bad = false;
+  for (int j = tid; j < r.nb; j += nthreads) bad |= r.bias_tok[j] < 0 || r.bias_tok[j] >= l.vocab;
+  if (bad) atomicOr(l.status, SSU_STATUS_BAD_BIAS);
+}
+
+// All stores of the workgroup have arrived, so that others to the same places come behind them.
+__device__ __forceinline__ void stores_done() {
+  __threadfence_block();
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  __syncthreads();
+}
 
 constexpr int kPieceThreads = 256;
+enum Mode { kStats, kProbs, kPlain };
 
-// MODE 0: statistics of a piece of a row into the workspace.  1: the probabilities of the
-// piece from them.  2: the piece's x / temperature.
-template <int IT, int OT, int G, int MODE>
+// A piece of a row, 8 values a thread.  kStats: its statistics into the workspace; kProbs: its probabilities from those of
+// all pieces; kPlain: x / temperature.
+template <int IT, int OT, Mode MODE>
 __global__ __launch_bounds__(kPieceThreads) void logits_piece_kernel(KHistory h, KLogits l, int pieces) {
-  constexpr int NT = kPieceThreads, PIECE = NT * 8 * G;
-  typedef Special<NT, PIECE / 32, PIECE> Sp;
+  constexpr int NT = kPieceThreads;
+  typedef Special<NT, kLogitsPiece / 32, kLogitsPiece> Sp;
+  static_assert(kLogitsPiece == NT * 8, "8 values a thread");
   __shared__ Sp sp;
   __shared__ Stat red[NT / 64];
   const int tid = threadIdx.x, piece = blockIdx.x, b = blockIdx.y / l.T, t = blockIdx.y - b * l.T;
   Row r;
-  if (!find_row(h, l, b, t, piece == 0 && tid == 0 && MODE != 1, r)) return;
-  const int i0 = piece * PIECE;
-  Eight<IT> e[G];
-#pragma unroll
-  for (int g = 0; g < G; ++g) {
-    const int i = i0 + (g * NT + tid) * 8;
-    if (i < l.vocab) e[g].load(r.in, i, l.vocab);
-  }
-  const bool greedy = is_greedy(r.temperature);
+  if (!find_row(h, l, b, t, piece == 0 && tid == 0 && MODE != kProbs, r)) return;
+  const int i0 = piece * kLogitsPiece, words = (min(kLogitsPiece, l.vocab - i0) + 31) / 32, i = i0 + tid * 8;
+  const bool full = i + 8 <= l.vocab, greedy = is_greedy(r.temperature);
+  Eight<IT> e;
+  if (full) e.load(r.in, i);
   const float k = slope(r.temperature);
+  uint8_t *out = l.out + r.row * l.out_stride;
   float2 *ws = l.ws + (int64_t)blockIdx.y * pieces;
-  Stat s = no_stat(greedy);
-  if constexpr (MODE == 1) {
+  Stat s = kNoStat;
+  Best best = kNoBest;
+  if constexpr (MODE == kProbs) {
     for (int j = tid; j < pieces; j += NT) {
       const float2 w = ws[j];
-      s = join(s, Stat{w.x, w.y}, k, greedy);
+      if (greedy)
+        best = better(best, Best{w.x, (int)__float_as_uint(w.y)});
+      else
+        s = join(s, Stat{w.x, w.y}, k);
     }
   }
-  const int total = sp.template build<IT>(r, i0, (min(PIECE, l.vocab - i0) + 31) / 32, l.vocab, tid);
-  if constexpr (MODE == 1) s = block_join<NT>(s, red, tid, k, greedy);
-  const float inv = inverse(s);
+  const int total = sp.mark(r, i0, words, l.vocab, tid);
+  if (total > 0) sp.template form<IT>(r, i0, words, l.vocab, 0, total, tid);
+  float v[8];
+  if (full) values8<IT>(e, sp.out8(tid * 8), v);
+  if (MODE != kPlain && greedy) {
+    if constexpr (MODE == kStats) {
+      if (full) {
 #pragma unroll
-  for (int g = 0; g < G; ++g) {
-    const int i = i0 + (g * NT + tid) * 8;
-    if (i >= l.vocab) continue;
-    float v[8];
-    sp.template values<IT>(r, e[g], total, i0, i, l.vocab, v);
-    if constexpr (MODE == 0) {
-      add8(s, v, i, k, greedy);
-    } else {
-      if constexpr (MODE == 1) {
-        probs8(v, i, s, inv, k, greedy);
-      } else if (!greedy) {
-#pragma unroll
-        for (int x = 0; x < 8; ++x) v[x] = v[x] / r.temperature;
+        for (int x = 0; x < 8; ++x) add_best(best, v[x], i + x);
       }
-      store8<OT>(l.out + r.row * l.out_stride, i, l.vocab, v);
+      for (int j = tid; j < total; j += NT) add_best(best, sp.x(j), i0 + (int)sp.token[j]);
+    }
+    best = block_best<NT>(best, reinterpret_cast<Best *>(red), tid);
+    if (MODE == kStats && tid == 0) ws[piece] = float2{best.m, __uint_as_float((uint32_t)best.i)};
+    if constexpr (MODE == kProbs) {
+#pragma unroll
+      for (int x = 0; x < 8; ++x) v[x] = i + x == best.i ? 1.f : 0.f;
+      if (full) store8<OT>(out, i, v, l.past);
+      if (!full) {
+        for (int x = 0; i + x < l.vocab; ++x) store1<OT>(out, i + x, i + x == best.i ? 1.f : 0.f);
+      }
+    }
+    s.m = best.m;
+  } else if constexpr (MODE == kStats) {
+    if (full) add_values<8>(s, v, k);
+    for (int j = tid; j < total; j += NT) {
+      const float x = sp.x(j);
+      add_values<1>(s, &x, k);
+    }
+    s = block_join<NT>(s, red, tid, k);
+    if (tid == 0) ws[piece] = float2{s.m, s.s};
+  } else {
+    if constexpr (MODE == kProbs) s = block_join<NT>(s, red, tid, k);
+    const Probs p(s, k);
+    auto result = [&](float x) {
+      if constexpr (MODE == kProbs) return p(x);
+      const float y = x == x ? x : -INFINITY;
+      return greedy ? y : y / r.temperature;
+    };
+    if (full) {
+#pragma unroll
+      for (int x = 0; x < 8; ++x) v[x] = result(v[x]);
+      store8<OT>(out, i, v, l.past);
+    }
+    if (total > 0) stores_done();
+    for (int j = tid; j < total; j += NT) store1<OT>(out, i0 + (int)sp.token[j], result(sp.x(j)));
+  }
+  if (MODE == kProbs && piece == 0 && tid == 0 && l.status && !(s.m > -INFINITY)) atomicOr(l.status, SSU_STATUS_EMPTY_ROW);
+  if (MODE != kProbs && piece == 0 && l.status && r.nb > 0 && t == 0) bad_biases(r, l, tid, NT);
+}
+
+// A whole row by one workgroup, two of 16 waves a CU: enough loads on their way while the other one lists its special
+// tokens.  The first HOLD groups of 8 values a thread are loaded before anything else and stay in registers, the others
+// are read AHEAD at a time, and for the second time from the caches.  (512 threads and 16 groups held took 318 us for 289 with
+// 1536 rows of 131072, one group at a time 304.)
+constexpr int kRowThreads = 1024, kRowMax = 131072;
+
+template <int IT, int OT>
+__global__ __launch_bounds__(kRowThreads, 8) void logits_row_kernel(KHistory h, KLogits l) {
+  constexpr int NT = kRowThreads, GROUP = NT * 8, HOLD = IT == kLF32 ? 2 : 4, AHEAD = HOLD / 2, CAP = 4096;
+  typedef Special<NT, kRowMax / 32, CAP> Sp;
+  __shared__ Sp sp;
+  __shared__ Stat red[NT / 64];
+  const int tid = threadIdx.x, b = blockIdx.x / l.T, t = blockIdx.x - b * l.T;
+  Row r;
+  if (!find_row(h, l, b, t, tid == 0, r)) return;
+  const int vocab = l.vocab, words = (vocab + 31) / 32, whole = vocab & ~7;
+  const float k = slope(r.temperature);
+  uint8_t *out = l.out + r.row * l.out_stride;
+  const int total = sp.mark(r, 0, words, vocab, tid);
+  // the special tokens, as many at a time as LDS has room for
+  auto special = [&](auto use) {
+    for (int first = 0; first < total; first += CAP) {
+      const int n = min(CAP, total - first);
+      sp.template form<IT>(r, 0, words, vocab, first, n, tid);
+      for (int j = tid; j < n; j += NT) use(sp.x(j), (int)sp.token[j]);
+      if (total > CAP) __syncthreads();
+    }
+  };
+  if (l.status && r.nb > 0 && t == 0) bad_biases(r, l, tid, NT);
+  if (is_greedy(r.temperature)) {
+    Best best = kNoBest;
+    special([&](float x, int i) { add_best(best, x, i); });
+    for (int i = tid * 8; i < whole; i += GROUP) {
+      Eight<IT> w;
+      w.load(r.in, i);
+      float v[8];
+      values8<IT>(w, sp.out8(i), v);
+#pragma unroll
+      for (int x = 0; x < 8; ++x) add_best(best, v[x], i + x);
+    }
+    best = block_best<NT>(best, reinterpret_cast<Best *>(red), tid);
+    for (int i = tid * 8; i < whole; i += GROUP) {
+      float v[8];
+#pragma unroll
+      for (int x = 0; x < 8; ++x) v[x] = i + x == best.i ? 1.f : 0.f;
+      store8<OT>(out, i, v, l.past);
+    }
+    if (tid < vocab - whole) store1<OT>(out, whole + tid, whole + tid == best.i ? 1.f : 0.f);
+    if (tid == 0 && l.status && !(best.m > -INFINITY)) atomicOr(l.status, SSU_STATUS_EMPTY_ROW);
+    return;
+  }
+  Eight<IT> e[HOLD];
+#pragma unroll
+  for (int g = 0; g < HOLD; ++g) {
+    const int i = g * GROUP + tid * 8;
+    if (i < whole) e[g].load(r.in, i);
+  }
+  Stat s = kNoStat;
+  special([&](float x, int) { add_values<1>(s, &x, k); });
+  auto groups = [&](auto use) {
+#pragma unroll
+    for (int g = 0; g < HOLD; ++g) {
+      const int i = g * GROUP + tid * 8;
+      if (i < whole) use(e[g], i);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    for (int i0 = HOLD * GROUP + tid * 8; i0 < whole; i0 += AHEAD * GROUP) {
+      Eight<IT> w[AHEAD];
+#pragma unroll
+      for (int a = 0; a < AHEAD; ++a)
+        if (i0 + a * GROUP < whole) w[a].load(r.in, i0 + a * GROUP);
+#pragma unroll
+      for (int a = 0; a < AHEAD; ++a) {
+        if (i0 + a * GROUP < whole) use(w[a], i0 + a * GROUP);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+  };
+  groups([&](const Eight<IT> &w, int i) {
+    float v[8];
+    values8<IT>(w, sp.out8(i), v);
+    add_values<8>(s, v, k);
+  });
+  s = block_join<NT>(s, red, tid, k);
+  const Probs p(s, k);
+#pragma unroll
+  for (int g = 0; g < HOLD; ++g) e[g].again();
+  // Where the list is not all of them, the special ones are formed again and written first (their logits may lie where the
+  // probabilities go), and the others around them.
+  if (total > CAP) {
+    special([&](float x, int i) { store1<OT>(out, i, p(x)); });
+    groups([&](const Eight<IT> &w, int i) {
+      float v[8];
+      values8<IT>(w, sp.out8(i), v);
+      const uint32_t around = (sp.bits[i >> 5] >> (i & 31)) & 255u;
+#pragma unroll
+      for (int x = 0; x < 8; ++x)
+        if (!((around >> x) & 1u)) store1<OT>(out, i + x, p(v[x]));
+    });
+  } else {
+    groups([&](const Eight<IT> &w, int i) {
+      float v[8];
+      values8<IT>(w, sp.out8(i), v);
+#pragma unroll
+      for (int x = 0; x < 8; ++x) v[x] = p(v[x]);
+      store8<OT>(out, i, v, l.past);
+    });
+    if (total > 0) {
+      stores_done();
+      for (int j = tid; j < total; j += NT) store1<OT>(out, (int)sp.token[j], p(sp.x(j)));
     }
   }
-  if constexpr (MODE == 0) {
-    s = block_join<NT>(s, red, tid, k, greedy);
-    if (tid == 0) ws[piece] = float2{s.m, s.s};
-  }
-  if (MODE == 1 && piece == 0 && tid == 0 && l.status && !(s.m > -INFINITY)) atomicOr(l.status, SSU_STATUS_EMPTY_ROW);
-  if (MODE != 1 && piece == 0 && l.status && r.nb > 0 && t == 0) {
-    bool bad = false;
-    for (int j = tid; j < r.nb; j += NT) bad |= r.bias_tok[j] < 0 || r.bias_tok[j] >= l.vocab;
-    if (bad) atomicOr(l.status, SSU_STATUS_BAD_BIAS);
-  }
+  if (tid == 0 && l.status && !(s.m > -INFINITY)) atomicOr(l.status, SSU_STATUS_EMPTY_ROW);
 }
 
 template <int IT, int OT>
 hipError_t logits_t(const KHistory &h, const KLogits &l, bool softmax, hipStream_t st) {
-  constexpr int G = 1;
-  const int pieces = (l.vocab + kPieceThreads * 8 * G - 1) / (kPieceThreads * 8 * G);
-  const dim3 grid((unsigned)pieces, (unsigned)(l.batch * l.T)), block(kPieceThreads);
+  const int pieces = (l.vocab + kLogitsPiece - 1) / kLogitsPiece, rows = l.batch * l.T;
+  const dim3 grid((unsigned)pieces, (unsigned)rows), block(kPieceThreads);
   if (!softmax) {
-    logits_piece_kernel<IT, OT, G, 2><<<grid, block, 0, st>>>(h, l, pieces);
+    logits_piece_kernel<IT, OT, kPlain><<<grid, block, 0, st>>>(h, l, pieces);
     return hipGetLastError();
   }
-  logits_piece_kernel<IT, kLF32, G, 0><<<grid, block, 0, st>>>(h, l, pieces);
+  // One launch against two and a read more, with 131072 bf16 values a row (f32 out) 64 rows 38.5 : 38.6 us, 32 rows 34 : 23,
+  // 256 rows 54 : 116; with 32000 32 rows 15.7 : 15.8, 1 row 14.3 : 13.0; with 8000 1 row 11.7 : 13.4, 64 rows 13.0 : 15.8.
+  if (l.vocab <= kRowMax && (rows >= pieces || l.vocab <= 16384)) {
+    logits_row_kernel<IT, OT><<<dim3((unsigned)rows), dim3(kRowThreads), 0, st>>>(h, l);
+    return hipGetLastError();
+  }
+  logits_piece_kernel<IT, kLF32, kStats><<<grid, block, 0, st>>>(h, l, pieces);
   const hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;
-  logits_piece_kernel<IT, OT, G, 1><<<grid, block, 0, st>>>(h, l, pieces);
+  logits_piece_kernel<IT, OT, kProbs><<<grid, block, 0, st>>>(h, l, pieces);
   return hipGetLastError();
 }
 
@@ -534,7 +735,9 @@ hipError_t logits_it(const KHistory &h, const KLogits &l, int out_type, bool sof
 }  // namespace
 
 hipError_t launch_count(const KHistory &h, const KCount &c, hipStream_t st) {
-  if (!c.reset && !c.cu && c.T <= 64)
+  if (c.prompt && h.words <= kPromptWords)
+    count_prompt_kernel<1024><<<dim3((unsigned)c.batch), dim3(1024), 0, st>>>(h, c);
+  else if (!c.reset && !c.cu && c.T <= 64)
     count_kernel<64><<<dim3((unsigned)c.batch), dim3(64), 0, st>>>(h, c);
   else
     count_kernel<1024><<<dim3((unsigned)c.batch), dim3(1024), 0, st>>>(h, c);
