@@ -590,12 +590,13 @@ __global__ __launch_bounds__(kPieceThreads) void logits_piece_kernel(KHistory h,
 // A whole row by one workgroup, two of 16 waves a CU: enough loads on their way while the other one lists its special
 // tokens.  The first HOLD groups of 8 values a thread are loaded before anything else and stay in registers, the others
 // are read AHEAD at a time, and for the second time from the caches.  (512 threads and 16 groups held took 318 us for 289 with
-// 1536 rows of 131072, one group at a time 304.)
-constexpr int kRowThreads = 1024, kRowMax = 131072;
+// 1536 rows of 131072, one group at a time 304.)  ALONE: no more rows than CUs, and twice the registers for loads on
+// their way (256 rows of 100003 fp32 values that no cache holds 75 -> 63 us; 16-bit ones the same as without).
+constexpr int kRowThreads = 1024, kRowMax = 131072, kAlone = 256;
 
-template <int IT, int OT>
-__global__ __launch_bounds__(kRowThreads, 8) void logits_row_kernel(KHistory h, KLogits l) {
-  constexpr int NT = kRowThreads, GROUP = NT * 8, HOLD = IT == kLF32 ? 2 : 4, AHEAD = HOLD / 2, CAP = 4096;
+template <int IT, int OT, bool ALONE>
+__global__ __launch_bounds__(kRowThreads, ALONE ? 4 : 8) void logits_row_kernel(KHistory h, KLogits l) {
+  constexpr int NT = kRowThreads, GROUP = NT * 8, HOLD = ALONE ? 8 : IT == kLF32 ? 2 : 4, AHEAD = HOLD / 2, CAP = 4096;
   typedef Special<NT, kRowMax / 32, CAP> Sp;
   __shared__ Sp sp;
   __shared__ Stat red[NT / 64];
@@ -713,7 +714,10 @@ hipError_t logits_t(const KHistory &h, const KLogits &l, bool softmax, hipStream
   // One launch against two and a read more, with 131072 bf16 values a row (f32 out) 64 rows 38.5 : 38.6 us, 32 rows 34 : 23,
   // 256 rows 54 : 116; with 32000 32 rows 15.7 : 15.8, 1 row 14.3 : 13.0; with 8000 1 row 11.7 : 13.4, 64 rows 13.0 : 15.8.
   if (l.vocab <= kRowMax && (rows >= pieces || l.vocab <= 16384)) {
-    logits_row_kernel<IT, OT><<<dim3((unsigned)rows), dim3(kRowThreads), 0, st>>>(h, l);
+    if (rows <= kAlone)
+      logits_row_kernel<IT, OT, true><<<dim3((unsigned)rows), dim3(kRowThreads), 0, st>>>(h, l);
+    else
+      logits_row_kernel<IT, OT, false><<<dim3((unsigned)rows), dim3(kRowThreads), 0, st>>>(h, l);
     return hipGetLastError();
   }
   logits_piece_kernel<IT, kLF32, kStats><<<grid, block, 0, st>>>(h, l, pieces);
