@@ -84,8 +84,8 @@ typedef struct ssu_prefill_args {
 } ssu_prefill_args;
 
 /* Bytes of scratch for `rows` rows in num_seqs sequences, whatever their
- * lengths (0, with the reason in ssu_last_error, for sizes outside the limits
- * above). */
+ * lengths; it is enough for fewer of both (0, with the reason in ssu_last_error,
+ * for sizes outside the limits above). */
 size_t ssu_prefill_workspace_size(int32_t rows, int32_t num_seqs, int32_t nheads);
 int ssu_prefill(const ssu_prefill_args *args, hipStream_t stream);
 

@@ -4,14 +4,20 @@
 //   y_t = e^(G_t) C_t.S + sum_(s <= t) W_ts x_s,
 //   W_ts = e^(G_t - G_s) dt'_s (C_t.B_s), + D on the diagonal,
 //   S' = e^(G_w) S + sum_s (e^(G_w - G_s) dt'_s x_s) B_s^T.
-// C.B is shared by the heads of a group.  A workgroup takes HPW heads of a
-// group, two waves a head: 32 of its 64 columns each, their state in registers
-// as matrix results [n][p], which are the next product's operand as they lie.
-// B, C and x of a chunk lie in LDS, the next chunk's on their way.
+// Everything but the exponentials is matrix products: a chunk and a head cost 128 (three
+// parts: 192) products of 16 x 16 x 32 for the readout, 192 for the update, 40 or 60 for the
+// tokens of the chunk and 40 for C.B, which the heads of a workgroup share.  Their operands
+// that are not bf16 have to be split into bf16 parts on the way, and that and the weights
+// cost the vector units as much again: 8 prompts of 2048 to 4096 tokens of 128 heads take
+// 400 us, 187 are their bytes, 125 the products alone.
+// Two waves a head have 32 of its 64 columns each (or four have 16), the state in registers
+// as matrix results [n][p], which are the next product's operand as they lie.  B, C and x of a
+// chunk lie in LDS, the next chunk's on their way in registers.
 //
 // Long sequences are cut into segments: prefill_kernel<.., true> forms what each
 // segment but the last adds to the state and its decay, segment_kernel the state that
-// each starts from, then all segments run at once.
+// each starts from, then all segments run at once (16384 tokens of 64 heads: 60, 13 and
+// 160 of 233 us).
 #include <algorithm>
 
 #include "delta_device.cuh"
@@ -24,7 +30,7 @@ namespace {
 constexpr int kT = kPChunk / 16;              // token tiles of a chunk
 constexpr int kTiles = kT * (kT + 1) / 2;     // C.B tiles on and below the diagonal
 constexpr int kHeadValues = kHeadDim * kDState;
-constexpr int kAhead = 2;                     // chunks whose gates are formed at once, one by each of a head's waves
+constexpr int head_waves(int CT) { return kT / CT; }  // of a head, 16 CT columns each: they form the gates of as many chunks at once
 
 constexpr int out_parts(int OT) { return OT == kOutF32 ? 3 : 2; }
 
@@ -214,10 +220,11 @@ __device__ __forceinline__ float gated(float v, float z) {
 // A chunk's rows on their way from memory to LDS through the registers of NT
 // threads; rows behind the segment's last repeat it (their dt' is 0), heads
 // behind the group's last repeat that.  Every load is unconditional.
-template <int HPW, bool STATE>
+template <int HPW, int CT, bool STATE>
 struct PStage {
-  static constexpr int NT = HPW * 128, NB = kPChunk * kDState / 8 / NT, NX = kPChunk * kHeadDim / 8 / 128;
-  static constexpr int RB = NT / (kDState / 8), RX = 16;  // rows that a step of all threads covers
+  static constexpr int NT = HPW * head_waves(CT) * 64;
+  static constexpr int RB = NT / (kDState / 8), RX = NT / (HPW * kHeadDim / 8);  // rows that a step of all threads covers
+  static constexpr int NB = kPChunk / RB, NX = kPChunk / RX;
   u32x4 b[NB], c[STATE ? 1 : NB], x[NX];
   // uniform bases of the segment's first row, bytes between rows
   const char *Bp, *Cp, *xp;
@@ -264,16 +271,16 @@ struct PStage {
 // Lane (m, q) of a wave holds of the state column p = p0 + 16 pt + m, values n =
 // 32 i + 8 q + 4 a + r in S[pt][i][a][r]; of the outputs row p0 + 16 pt + 4 q + r,
 // token 16 ti + m in y[pt][ti][r].
-template <int OT, int HPW, bool STATE, bool GATE>
-__global__ __launch_bounds__(HPW * 128, HPW) void prefill_kernel(KPrefill p, int htiles, int unit, int64_t ntiles) {
-  constexpr int NP = out_parts(OT);
+template <int OT, int HPW, int CT, bool STATE, bool GATE>
+__global__ __launch_bounds__(HPW * head_waves(CT) * 64, HPW * head_waves(CT) / 2) void prefill_kernel(KPrefill p, int htiles, int unit, int64_t ntiles) {
+  constexpr int NP = out_parts(OT), WPH = head_waves(CT), NT = HPW * WPH * 64;
   __shared__ PBuf<HPW, STATE> in;
-  __shared__ __align__(16) Gates gates[HPW][kAhead];
+  __shared__ __align__(16) Gates gates[HPW][WPH];
   __shared__ f32x4 cb[STATE ? 1 : kTiles][64];
   const int tid = threadIdx.x, lane = tid & 63, m = lane & 15, q = lane >> 4;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), hh = wave >> 1, p0 = (wave & 1) * 32;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), hh = wave / WPH, wh = wave % WPH, p0 = wh * 16 * CT;
   if (!STATE) {
-    for (int64_t s = (int64_t)blockIdx.x * (HPW * 128) + tid; s < p.n; s += (int64_t)gridDim.x * (HPW * 128)) {
+    for (int64_t s = (int64_t)blockIdx.x * NT + tid; s < p.n; s += (int64_t)gridDim.x * NT) {
       int b0, b1;
       if (!seq_rows(p, (int)s, b0, b1) && p.status) atomicOr(p.status, SSU_STATUS_BAD_SEQLEN);
     }
@@ -301,11 +308,11 @@ __global__ __launch_bounds__(HPW * 128, HPW) void prefill_kernel(KPrefill p, int
   const bool on = hh < heads;
   const int h = hfirst + min(hh, heads - 1);
 
-  f32x4 S[2][4][2];
+  f32x4 S[CT][4][2];
   const int64_t own = (int64_t)h * kHeadValues + (p0 + m) * kDState + 8 * q;  // of (i, a, pt) = 0
   const float *from = STATE ? nullptr : (sg.n > 1 ? p.ws + (int64_t)slot * p.H * kHeadValues : p.h0 ? p.h0 + (int64_t)sg.seq * p.H * kHeadValues : nullptr);
 #pragma unroll
-  for (int pt = 0; pt < 2; ++pt)
+  for (int pt = 0; pt < CT; ++pt)
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -315,7 +322,7 @@ __global__ __launch_bounds__(HPW * 128, HPW) void prefill_kernel(KPrefill p, int
   if (chunks > 0) {
     const float A = p.A[h], bias = p.dt_bias[h], D = STATE ? 0.f : p.D[h];
     double total = 0.0;
-    PStage<HPW, STATE> st;
+    PStage<HPW, CT, STATE> st;
     auto last_of = [&](int c) { return min(kPChunk, rows - c * kPChunk) - 1; };
     // tokens of chunk c (0: there is none), and their dt
     auto there_of = [&](int c) { return max(0, min(kPChunk, rows - c * kPChunk)); };
@@ -327,7 +334,7 @@ __global__ __launch_bounds__(HPW * 128, HPW) void prefill_kernel(KPrefill p, int
     const char *zp = GATE ? reinterpret_cast<const char *>(p.z + row0 * p.z_stride) : nullptr;
     st.begin(p, row0, g, hfirst, heads);
     st.fetch(0, last_of(0), tid);
-    float dt = dt_of(wave & 1);
+    float dt = dt_of(wh);
     for (int c = 0; c < chunks; ++c) {
       // The lane's addresses are formed again in every chunk: held from one to the next they would spill.
       int thread = tid;
@@ -337,39 +344,40 @@ __global__ __launch_bounds__(HPW * 128, HPW) void prefill_kernel(KPrefill p, int
       char *out = static_cast<char *>(p.out) + (row0 + c * kPChunk) * os;
       __syncthreads();
       st.store(in, thread);
-      if (c % kAhead == 0) {  // the gates of the next two chunks, one by each of the head's waves
-        const int c0 = c + (wave & 1);
-        total += write_gates<STATE>(gates[hh][wave & 1], dt, bias, A, p.softplus, there_of(c0), lane);
-        dt = dt_of(c0 + kAhead);
+      if (c % WPH == 0) {  // the gates of the next chunks, one by each of the head's waves
+        const int c0 = c + wh;
+        total += write_gates<STATE>(gates[hh][wh], dt, bias, A, p.softplus, there_of(c0), lane);
+        dt = dt_of(c0 + WPH);
       }
       __syncthreads();
-      const Gates &gt = gates[hh][c % kAhead];
-      u32x2 zw[2][kT];
+      const Gates &gt = gates[hh][c % WPH];
+      u32x2 zw[CT][kT];
       if constexpr (GATE) {
         const char *z = zp + (int64_t)c * kPChunk * zs;
         const uint32_t zch = (h * kHeadDim + p0 + 4 * q) * 2;
 #pragma unroll
         for (int ti = 0; ti < kT; ++ti)
 #pragma unroll
-          for (int pt = 0; pt < 2; ++pt) zw[pt][ti] = ld8(z + (uint32_t)(min(m * zs + 16 * ti * zs, (W - 1) * zs) + zch) + 32 * pt);
+          for (int pt = 0; pt < CT; ++pt) zw[pt][ti] = ld8(z + (uint32_t)(min(m * zs + 16 * ti * zs, (W - 1) * zs) + zch) + 32 * pt);
       }
-      bf16x8 xf[2][2];
+      bf16x8 xf[CT][2];
 #pragma unroll
-      for (int pt = 0; pt < 2; ++pt)
+      for (int pt = 0; pt < CT; ++pt)
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks) xf[pt][ks] = x_tile(in.x[hh], ks, p0 + 16 * pt, lane);
-      f32x4 y[2][kT];
+      f32x4 y[CT][kT];
       if constexpr (!STATE) {
         // The state's readout, and beside it C.B of token tiles si with all (those above the diagonal are not used).
         // What a step reads from LDS is read a step ahead.
-        constexpr int NS = 2 / HPW;
+        constexpr int NS = kT / (HPW * WPH);
         int si[NS];
 #pragma unroll
         for (int k = 0; k < NS; ++k) si[k] = k == 0 ? wave : 3 - wave;
         f32x4 v[NS][kT];
 #pragma unroll
         for (int ti = 0; ti < kT; ++ti) {
-          y[0][ti] = y[1][ti] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int pt = 0; pt < CT; ++pt) y[pt][ti] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int k = 0; k < NS; ++k) v[k][ti] = f32x4{0.f, 0.f, 0.f, 0.f};
         }
@@ -385,9 +393,9 @@ __global__ __launch_bounds__(HPW * 128, HPW) void prefill_kernel(KPrefill p, int
         for (int i = 0; i < 4; ++i) {
           if (i < 3) read(i + 1);
           __builtin_amdgcn_sched_barrier(0);
-          bf16x8 f[2][NP];
+          bf16x8 f[CT][NP];
 #pragma unroll
-          for (int pt = 0; pt < 2; ++pt) {
+          for (int pt = 0; pt < CT; ++pt) {
             const float s[8] = {S[pt][i][0][0], S[pt][i][0][1], S[pt][i][0][2], S[pt][i][0][3],
                                 S[pt][i][1][0], S[pt][i][1][1], S[pt][i][1][2], S[pt][i][1][3]};
             split<NP>(s, f[pt]);
@@ -401,7 +409,7 @@ __global__ __launch_bounds__(HPW * 128, HPW) void prefill_kernel(KPrefill p, int
 #pragma unroll
             for (int ti = 0; ti < kT; ++ti)
 #pragma unroll
-              for (int pt = 0; pt < 2; ++pt) y[pt][ti] = mfma_bf16(f[pt][a], cf[i & 1][ti], y[pt][ti]);
+              for (int pt = 0; pt < CT; ++pt) y[pt][ti] = mfma_bf16(f[pt][a], cf[i & 1][ti], y[pt][ti]);
         }
 #pragma unroll
         for (int k = 0; k < NS; ++k)
@@ -412,13 +420,13 @@ __global__ __launch_bounds__(HPW * 128, HPW) void prefill_kernel(KPrefill p, int
       // S <- e^(G_w) S + B^T (w x)
       {
         st.fetch(next * kPChunk, last_of(next), thread);
-        bf16x8 xw[2][3], bt[3];
+        bf16x8 xw[CT][3], bt[3];
         auto read = [&](int j) { bt[j % 3] = b_tile(in.B, j >> 3, 32 * (j >> 1 & 3), j & 1, lane); };
         auto weigh = [&](int ks) {  // w x of tokens 32 ks .., in three parts
           const f32x4 w0 = *reinterpret_cast<const f32x4 *>(gt.w + 32 * ks + 4 * q);
           const f32x4 w1 = *reinterpret_cast<const f32x4 *>(gt.w + 32 * ks + 16 + 4 * q);
 #pragma unroll
-          for (int pt = 0; pt < 2; ++pt) {
+          for (int pt = 0; pt < CT; ++pt) {
             const u32x4 xx = __builtin_bit_cast(u32x4, xf[pt][ks]);
             float v[8];
 #pragma unroll
@@ -437,12 +445,12 @@ __global__ __launch_bounds__(HPW * 128, HPW) void prefill_kernel(KPrefill p, int
           __builtin_amdgcn_sched_barrier(0);
           if (ks == 0) {
 #pragma unroll
-            for (int pt = 0; pt < 2; ++pt) S[pt][i][a] = scale4(S[pt][i][a], ew);
+            for (int pt = 0; pt < CT; ++pt) S[pt][i][a] = scale4(S[pt][i][a], ew);
           }
 #pragma unroll
           for (int k = 2; k >= 0; --k)
 #pragma unroll
-            for (int pt = 0; pt < 2; ++pt) S[pt][i][a] = mfma_bf16(bt[j % 3], xw[pt][k], S[pt][i][a]);
+            for (int pt = 0; pt < CT; ++pt) S[pt][i][a] = mfma_bf16(bt[j % 3], xw[pt][k], S[pt][i][a]);
         }
       }
       if constexpr (!STATE) {
@@ -454,7 +462,7 @@ __global__ __launch_bounds__(HPW * 128, HPW) void prefill_kernel(KPrefill p, int
           const int t = 16 * ti + m;
           const float e = gt.e[t], hi = gt.hi[t], lo = gt.lo[t], row = gt.row[t];
 #pragma unroll
-          for (int pt = 0; pt < 2; ++pt) y[pt][ti] = scale4(y[pt][ti], e);
+          for (int pt = 0; pt < CT; ++pt) y[pt][ti] = scale4(y[pt][ti], e);
 #pragma unroll
           for (int ks = 0; ks <= ti / 2; ++ks) {
             float w[8];
@@ -486,11 +494,11 @@ __global__ __launch_bounds__(HPW * 128, HPW) void prefill_kernel(KPrefill p, int
 #pragma unroll
             for (int a = NP - 1; a >= 0; --a)
 #pragma unroll
-              for (int pt = 0; pt < 2; ++pt) y[pt][ti] = mfma_bf16(xf[pt][ks], wf[a], y[pt][ti]);
+              for (int pt = 0; pt < CT; ++pt) y[pt][ti] = mfma_bf16(xf[pt][ks], wf[a], y[pt][ti]);
           }
           if (on && t < W) {
 #pragma unroll
-            for (int pt = 0; pt < 2; ++pt) {
+            for (int pt = 0; pt < CT; ++pt) {
               f32x4 v = y[pt][ti];
               if (GATE) {
 #pragma unroll
@@ -509,15 +517,20 @@ __global__ __launch_bounds__(HPW * 128, HPW) void prefill_kernel(KPrefill p, int
     if constexpr (STATE) {  // each wave has summed the chunks it formed
       __syncthreads();
       double *sum = reinterpret_cast<double *>(&gates[hh][0]);
-      if (lane == 0) sum[wave & 1] = total;
+      if (lane == 0) sum[wh] = total;
       __syncthreads();
-      if ((wave & 1) == 0 && lane == 0 && on) p.decay[(int64_t)slot * p.H + h] = sum[0] + sum[1];
+      if (wh == 0 && lane == 0 && on) {
+        total = sum[0];
+#pragma unroll
+        for (int k = 1; k < WPH; ++k) total += sum[k];
+        p.decay[(int64_t)slot * p.H + h] = total;
+      }
     }
   }
   float *to = STATE ? p.ws + (int64_t)slot * p.H * kHeadValues : (p.h1 && sg.i == sg.n - 1 ? p.h1 + (int64_t)sg.seq * p.H * kHeadValues : nullptr);
   if (!to || !on) return;
 #pragma unroll
-  for (int pt = 0; pt < 2; ++pt)
+  for (int pt = 0; pt < CT; ++pt)
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -549,14 +562,14 @@ __global__ __launch_bounds__(256) void segment_kernel(KPrefill p) {
   }
 }
 
-template <int HPW>
-hipError_t prefill_hpw(const KPrefill &p, int out_type, hipStream_t st) {
+template <int HPW, int CT>
+hipError_t prefill_t(const KPrefill &p, int out_type, hipStream_t st) {
   const int htiles = p.G * ((p.hpg + HPW - 1) / HPW);
   const int64_t ntiles = prefill_slots(p.rows, p.n, p.seg) * htiles;
   const int per_group = htiles / p.G, unit = per_group % 4 == 0 ? 4 : per_group % 2 == 0 ? 2 : 1;
-  const dim3 grid((unsigned)((ntiles + 8 * unit - 1) / (8 * unit) * (8 * unit))), block(HPW * 128);
+  const dim3 grid((unsigned)((ntiles + 8 * unit - 1) / (8 * unit) * (8 * unit))), block(HPW * head_waves(CT) * 64);
   if (p.rows > 2 * (int64_t)p.seg) {  // a sequence may have two
-    prefill_kernel<kOutF32, HPW, true, false><<<grid, block, 0, st>>>(p, htiles, unit, ntiles);
+    prefill_kernel<kOutF32, HPW, CT, true, false><<<grid, block, 0, st>>>(p, htiles, unit, ntiles);
     hipError_t err = hipGetLastError();
     if (err != hipSuccess) return err;
     segment_kernel<<<dim3((unsigned)((int64_t)p.n * p.H * (kHeadValues / 1024))), dim3(256), 0, st>>>(p);
@@ -564,28 +577,40 @@ hipError_t prefill_hpw(const KPrefill &p, int out_type, hipStream_t st) {
     if (err != hipSuccess) return err;
   }
   if (out_type == kOutF32 && p.z)
-    prefill_kernel<kOutF32, HPW, false, true><<<grid, block, 0, st>>>(p, htiles, unit, ntiles);
+    prefill_kernel<kOutF32, HPW, CT, false, true><<<grid, block, 0, st>>>(p, htiles, unit, ntiles);
   else if (out_type == kOutF32)
-    prefill_kernel<kOutF32, HPW, false, false><<<grid, block, 0, st>>>(p, htiles, unit, ntiles);
+    prefill_kernel<kOutF32, HPW, CT, false, false><<<grid, block, 0, st>>>(p, htiles, unit, ntiles);
   else if (p.z)
-    prefill_kernel<kOutBF16, HPW, false, true><<<grid, block, 0, st>>>(p, htiles, unit, ntiles);
+    prefill_kernel<kOutBF16, HPW, CT, false, true><<<grid, block, 0, st>>>(p, htiles, unit, ntiles);
   else
-    prefill_kernel<kOutBF16, HPW, false, false><<<grid, block, 0, st>>>(p, htiles, unit, ntiles);
+    prefill_kernel<kOutBF16, HPW, CT, false, false><<<grid, block, 0, st>>>(p, htiles, unit, ntiles);
   return hipGetLastError();
 }
 
 }  // namespace
 
-// Tokens of a segment: as many as leave two workgroups of two heads to each CU.
+// Tokens of a segment: as many as leave two workgroups of two heads to each CU, and at least so many that the pass before
+// it pays: 256 where there are few workgroups (one prompt of 64 heads, 384 : 256: 2000 tokens 68 : 58 us, 4000 100 : 85), more
+// otherwise (16 of 351 to 701 tokens, 32 heads, 75 : 96; 8 of them 57 : 75; 4 of them 53 : 54).
 int prefill_segment(int64_t rows, int64_t n, int64_t heads) {
-  (void)n;
-  const int64_t want = (rows * ((heads + 1) / 2) + 511) / 512;
-  return (int)((std::max<int64_t>(want, 384) + kPChunk - 1) / kPChunk * kPChunk);
+  const int64_t pairs = (heads + 1) / 2, want = (rows * pairs + 511) / 512, least = n * pairs <= 64 ? kLeastSegment : 384;
+  return (int)((std::max<int64_t>(want, least) + kPChunk - 1) / kPChunk * kPChunk);
 }
 
+// The most slots of a call of up to so many rows and sequences.
+int64_t prefill_most_slots(int64_t rows, int64_t n, int64_t heads) {
+  return std::min<int64_t>(rows / kLeastSegment, 512 / ((heads + 1) / 2)) + n;
+}
+
+// Two heads a workgroup, which share B, C and their products, two waves of 32 columns each; where a CU would have no more
+// than one of those, and where a group has one head, a workgroup a head, four waves of 16 columns: one prompt of 500 tokens,
+// 64 heads, 49 : 35 us, 12 of 351 to 701 tokens, 32 heads, 75 : 61, 16 of them (256 workgroups of two heads) 80 : 75.
+// (Workgroups of one head of two waves: 8 prompts of 500 to 1000 tokens, 64 heads of 64 groups, 155 us for 138.)
 hipError_t launch_prefill(const KPrefill &p, int out_type, hipStream_t st) {
-  if (p.hpg >= 2) return prefill_hpw<2>(p, out_type, st);
-  return prefill_hpw<1>(p, out_type, st);
+  if (p.hpg < 2) return prefill_t<1, 1>(p, out_type, st);
+  const int64_t each = (p.rows + p.n - 1) / p.n, segments = each <= 2 * (int64_t)p.seg ? 1 : (each + p.seg - 1) / p.seg;
+  if (p.n * segments * p.G * ((p.hpg + 1) / 2) <= 256) return prefill_t<1, 1>(p, out_type, st);
+  return prefill_t<2, 2>(p, out_type, st);
 }
 
 }  // namespace ssu

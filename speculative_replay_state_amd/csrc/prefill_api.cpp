@@ -41,14 +41,9 @@ int check_sizes(int64_t rows, int64_t n, int64_t heads) {
   return SSU_OK;
 }
 
-// States of the segments, then their decays; none where no sequence can have two.
+// States of the segments, then their decays.
 size_t state_bytes(int64_t slots, int64_t heads) { return (size_t)(slots * heads * ssu::kHeadDim * ssu::kDState) * sizeof(float); }
-size_t bytes_for(int64_t rows, int64_t n, int64_t heads) {
-  const int64_t seg = ssu::prefill_segment(rows, n, heads);
-  if (rows <= 2 * seg) return 0;
-  const int64_t slots = ssu::prefill_slots(rows, n, seg);
-  return state_bytes(slots, heads) + (size_t)(slots * heads) * sizeof(double);
-}
+size_t bytes_for(int64_t slots, int64_t heads) { return state_bytes(slots, heads) + (size_t)(slots * heads) * sizeof(double); }
 
 int check_row_stride(const char *name, int64_t stride, int64_t packed) {
   if (stride < packed || stride % 8 != 0)
@@ -65,7 +60,8 @@ extern "C" {
 size_t ssu_prefill_workspace_size(int32_t rows, int32_t num_seqs, int32_t nheads) {
   if (check_sizes(rows, num_seqs, nheads) != SSU_OK) return 0;
   api_ok();
-  return bytes_for(rows, num_seqs, nheads);
+  // (of any call of up to as many rows and sequences; none where no sequence can have two segments)
+  return rows <= 2 * ssu::kLeastSegment ? 0 : bytes_for(ssu::prefill_most_slots(rows, num_seqs, nheads), nheads);
 }
 
 int ssu_prefill(const ssu_prefill_args *a, hipStream_t stream) {
@@ -97,7 +93,9 @@ int ssu_prefill(const ssu_prefill_args *a, hipStream_t stream) {
   if (rc == SSU_OK) rc = check_row_stride("C", a->C_row_stride, group);
   if (rc == SSU_OK && a->z) rc = check_row_stride("z", a->z_row_stride, inner);
   if (rc != SSU_OK) return rc;
-  const size_t need = bytes_for(a->rows, a->num_seqs, a->nheads);
+  const int seg = ssu::prefill_segment(a->rows, a->num_seqs, a->nheads);
+  const int64_t slots = a->rows <= 2 * (int64_t)seg ? 0 : ssu::prefill_slots(a->rows, a->num_seqs, seg);
+  const size_t need = bytes_for(slots, a->nheads);
   if (need > 0 && (!a->workspace || a->workspace_bytes < need))
     return api_fail(SSU_ERR_WORKSPACE, "the prefill needs a workspace of %zu bytes (got %zu%s)", need, a->workspace_bytes,
                     a->workspace ? "" : ", NULL");
@@ -108,7 +106,7 @@ int ssu_prefill(const ssu_prefill_args *a, hipStream_t stream) {
   p.H = a->nheads;
   p.G = a->ngroups;
   p.hpg = a->nheads / a->ngroups;
-  p.seg = ssu::prefill_segment(a->rows, a->num_seqs, a->nheads);
+  p.seg = seg;
   p.cu = a->cu_seqlens;
   p.x = static_cast<const uint16_t *>(a->x);
   p.B = static_cast<const uint16_t *>(a->B);
@@ -127,8 +125,7 @@ int ssu_prefill(const ssu_prefill_args *a, hipStream_t stream) {
   p.h1 = a->final_states;
   p.out = a->out;
   p.ws = static_cast<float *>(a->workspace);
-  p.decay = reinterpret_cast<double *>(static_cast<uint8_t *>(a->workspace) +
-                                       (need ? state_bytes(ssu::prefill_slots(a->rows, a->num_seqs, p.seg), a->nheads) : 0));
+  p.decay = reinterpret_cast<double *>(static_cast<uint8_t *>(a->workspace) + state_bytes(slots, a->nheads));
   p.status = a->status;
   const hipError_t err = ssu::launch_prefill(p, od == SSU_F32 ? ssu::kOutF32 : ssu::kOutBF16, stream);
   return err == hipSuccess ? api_ok() : api_fail(SSU_ERR_HIP, "kernel launch failed: %s", hipGetErrorString(err));

@@ -32,7 +32,9 @@ struct KPrefill {
 
 // Segment slots: sequence s has slots cu[s] / seg + s and on, as many as segments.
 inline int64_t prefill_slots(int64_t rows, int64_t n, int64_t seg) { return rows / seg + n; }
+constexpr int kLeastSegment = 256;
 int prefill_segment(int64_t rows, int64_t n, int64_t heads);
+int64_t prefill_most_slots(int64_t rows, int64_t n, int64_t heads);
 
 hipError_t launch_prefill(const KPrefill &p, int out_type, hipStream_t stream);
 hipError_t launch_read(const KCache &c, float *states, int64_t stride, const int32_t *slot_idx, int n, int state_type, int recur,
