@@ -303,7 +303,7 @@ struct Special {
   // By the whole workgroup: the bitmaps; the number of special tokens.
   __device__ __forceinline__ int mark(const Row &r, int i0, int words, int vocab, int tid) {
     const int end = min(i0 + 32 * words, vocab);
-    const bool some = r.seen || r.nd > 0 || r.nb > 0 || (vocab & 7);
+    const bool some = r.seen || r.nd > 0 || r.nb > 0 || (end == vocab && (vocab & 7));
     for (int w = tid; w < words; w += NT) {
       const int left = vocab - i0 - 32 * w;  // (> 0: the words are the vocabulary's)
       const uint32_t real = left < 32 ? (1u << left) - 1u : ~0u;
