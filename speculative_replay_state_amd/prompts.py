@@ -116,10 +116,10 @@ def read_state(cache: DeviceCache, states, slot_idx, recur=False, stream=None):
     if states.dtype != torch.float32:
         raise ValueError("states must be torch.float32 (got %s)" % states.dtype)
     _shape(states, "states", (n, cache.nheads, cache.headdim, cache.dstate))
-    if n and not states[0].is_contiguous():
-        raise ValueError("states: each entry must be contiguous")
     packed = cache.nheads * cache.headdim * cache.dstate
     stride = packed if n <= 1 else states.stride(0)
+    if n and not states.is_contiguous() and not states[0].is_contiguous():
+        raise ValueError("states: each entry must be contiguous")
     if stride < packed:
         raise ValueError("states: its entries overlap (%d elements apart, of %d)" % (stride, packed))
     device = _one_device({"state": cache.state, "states": states, "slot_idx": slot_idx})
