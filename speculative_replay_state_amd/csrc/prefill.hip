@@ -18,6 +18,8 @@
 // segment but the last adds to the state and its decay, segment_kernel the state that
 // each starts from, then all segments run at once (16384 tokens of 64 heads: 60, 13 and
 // 160 of 233 us).
+#include <stddef.h>
+
 #include <algorithm>
 
 #include "delta_device.cuh"
@@ -121,6 +123,10 @@ template <int HPW, bool STATE>
 struct PBuf {
   __align__(16) uint16_t B[kPChunk * kBcRow], C[STATE ? 8 : kPChunk * kBcRow], x[HPW][kPChunk * kHeadDim];
 };
+
+// The pairs of a chunk's tiles of 16 tokens ti with tiles of 32 ks that hold tokens up to them.
+constexpr int kPairs = 6;
+constexpr int pair_at(int ti, int ks) { return (ti < 2 ? ti : 2 * ti - 2) + ks; }
 
 // v of lane l
 __device__ __forceinline__ double lane_d(double v, int l) {
@@ -274,7 +280,10 @@ struct PStage {
 template <int OT, int HPW, int CT, bool STATE, bool GATE>
 __global__ __launch_bounds__(HPW * head_waves(CT) * 64, HPW * head_waves(CT) / 2) void prefill_kernel(KPrefill p, int htiles, int unit, int64_t ntiles) {
   constexpr int NP = out_parts(OT), WPH = head_waves(CT), NT = HPW * WPH * 64;
-  __shared__ PBuf<HPW, STATE> in;
+  typedef PBuf<HPW, STATE> Buf;
+  constexpr size_t kShareAt = offsetof(Buf, C);
+  constexpr bool SHARE = !STATE && kShareAt + HPW * kPairs * NP * 64 * sizeof(bf16x8) <= sizeof(Buf);
+  __shared__ Buf in;
   __shared__ __align__(16) Gates gates[HPW][WPH];
   __shared__ f32x4 cb[STATE ? 1 : kTiles][64];
   const int tid = threadIdx.x, lane = tid & 63, m = lane & 15, q = lane >> 4;
@@ -454,43 +463,74 @@ __global__ __launch_bounds__(HPW * head_waves(CT) * 64, HPW * head_waves(CT) / 2
         }
       }
       if constexpr (!STATE) {
+        // W of tokens 16 ti .. with 32 ks .., as the parts of an operand
+        auto weights = [&](int ti, int ks, bf16x8 (&wf)[NP]) {
+          const int t = 16 * ti + m;
+          float w[8];
+#pragma unroll
+          for (int a = 0; a < 2; ++a) {
+            const int si = 2 * ks + a, s0 = 16 * si + 4 * q;
+            if (si > ti) {
+#pragma unroll
+              for (int r = 0; r < 4; ++r) w[4 * a + r] = 0.f;
+              continue;
+            }
+            const f32x4 v = cb[ti * (ti + 1) / 2 + si][lane];
+            if (si < ti) {
+              const f32x4 col = *reinterpret_cast<const f32x4 *>(gt.col[ti - 1] + s0);
+              const float row = gt.row[t];
+#pragma unroll
+              for (int r = 0; r < 4; ++r) w[4 * a + r] = v[r] * col[r] * row;
+              continue;
+            }
+            const f32x4 shi = *reinterpret_cast<const f32x4 *>(gt.hi + s0), slo = *reinterpret_cast<const f32x4 *>(gt.lo + s0);
+            const f32x4 sdt = *reinterpret_cast<const f32x4 *>(gt.dt + s0);
+            const float hi = gt.hi[t], lo = gt.lo[t];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const float d = __builtin_amdgcn_exp2f((hi - shi[r]) + (lo - slo[r])) * sdt[r] * v[r];
+              w[4 * a + r] = 4 * q + r < m ? d : (4 * q + r == m ? d + D : 0.f);
+            }
+          }
+          split<NP>(w, wf);
+        };
+        // Where there is room behind C (which nobody reads any more), a head's waves form a part of W each (16 prompts of
+        // 351 to 701 tokens, 32 heads, 75 -> 70 us; 8 of 2048 to 4096, 128 heads, gated, 491 -> 479).
+        bf16x8 *shared = reinterpret_cast<bf16x8 *>(reinterpret_cast<uint8_t *>(&in) + kShareAt) + hh * kPairs * NP * 64 + lane;
         __syncthreads();
+        if constexpr (SHARE) {
+          auto form = [&](int ti) {
+#pragma unroll
+            for (int ks = 0; ks <= ti / 2; ++ks) {
+              bf16x8 wf[NP];
+              weights(ti, ks, wf);
+#pragma unroll
+              for (int a = 0; a < NP; ++a) shared[(pair_at(ti, ks) * NP + a) * 64] = wf[a];
+            }
+          };
+          if (wh == 0) form(0);
+          if (wh == 1) form(1);
+          if (wh == (CT == 2 ? 1 : 2)) form(2);
+          if (wh == (CT == 2 ? 0 : 3)) form(3);
+          __syncthreads();
+        }
         // the tokens of the chunk, and out
         const uint32_t och = (h * kHeadDim + p0 + 4 * q) * kOut;
 #pragma unroll
         for (int ti = 0; ti < kT; ++ti) {
           const int t = 16 * ti + m;
-          const float e = gt.e[t], hi = gt.hi[t], lo = gt.lo[t], row = gt.row[t];
+          const float e = gt.e[t];
 #pragma unroll
           for (int pt = 0; pt < CT; ++pt) y[pt][ti] = scale4(y[pt][ti], e);
 #pragma unroll
           for (int ks = 0; ks <= ti / 2; ++ks) {
-            float w[8];
-#pragma unroll
-            for (int a = 0; a < 2; ++a) {
-              const int si = 2 * ks + a, s0 = 16 * si + 4 * q;
-              if (si > ti) {
-#pragma unroll
-                for (int r = 0; r < 4; ++r) w[4 * a + r] = 0.f;
-                continue;
-              }
-              const f32x4 v = cb[ti * (ti + 1) / 2 + si][lane];
-              if (si < ti) {
-                const f32x4 col = *reinterpret_cast<const f32x4 *>(gt.col[ti - 1] + s0);
-#pragma unroll
-                for (int r = 0; r < 4; ++r) w[4 * a + r] = v[r] * col[r] * row;
-                continue;
-              }
-              const f32x4 shi = *reinterpret_cast<const f32x4 *>(gt.hi + s0), slo = *reinterpret_cast<const f32x4 *>(gt.lo + s0);
-              const f32x4 sdt = *reinterpret_cast<const f32x4 *>(gt.dt + s0);
-#pragma unroll
-              for (int r = 0; r < 4; ++r) {
-                const float d = __builtin_amdgcn_exp2f((hi - shi[r]) + (lo - slo[r])) * sdt[r] * v[r];
-                w[4 * a + r] = 4 * q + r < m ? d : (4 * q + r == m ? d + D : 0.f);
-              }
-            }
             bf16x8 wf[NP];
-            split<NP>(w, wf);
+            if constexpr (SHARE) {
+#pragma unroll
+              for (int a = 0; a < NP; ++a) wf[a] = shared[(pair_at(ti, ks) * NP + a) * 64];
+            } else {
+              weights(ti, ks, wf);
+            }
 #pragma unroll
             for (int a = NP - 1; a >= 0; --a)
 #pragma unroll
@@ -604,7 +644,7 @@ int64_t prefill_most_slots(int64_t rows, int64_t n, int64_t heads) {
 
 // Two heads a workgroup, which share B, C and their products, two waves of 32 columns each; where a CU would have no more
 // than one of those, and where a group has one head, a workgroup a head, four waves of 16 columns: one prompt of 500 tokens,
-// 64 heads, 49 : 35 us, 12 of 351 to 701 tokens, 32 heads, 75 : 61, 16 of them (256 workgroups of two heads) 80 : 75.
+// 64 heads, 49 : 35 us, 12 of 351 to 701 tokens, 32 heads, 75 : 58, 16 of them (256 workgroups of two heads) 80 : 70.
 // (Workgroups of one head of two waves: 8 prompts of 500 to 1000 tokens, 64 heads of 64 groups, 155 us for 138.)
 hipError_t launch_prefill(const KPrefill &p, int out_type, hipStream_t st) {
   if (p.hpg < 2) return prefill_t<1, 1>(p, out_type, st);
