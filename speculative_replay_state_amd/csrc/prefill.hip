@@ -587,6 +587,7 @@ __global__ __launch_bounds__(256) void segment_kernel(KPrefill p) {
   const int nseg = segments_of(p, b1 - b0);
   if (nseg < 2) return;
   const int64_t e = (int64_t)h * kHeadValues + part * 1024 + threadIdx.x * 4, slot0 = first_slot(p, seq, threadIdx.x & 63);
+  if (slot0 + nseg > prefill_slots(p.rows, p.n, p.seg)) return;  // (sequences that overlap have more segments than there are slots)
   f32x4 S = p.h0 ? *reinterpret_cast<const f32x4 *>(p.h0 + (int64_t)seq * p.H * kHeadValues + e) : f32x4{0.f, 0.f, 0.f, 0.f};
   for (int i = 0; i < nseg; ++i) {
     float *at = p.ws + (slot0 + i) * p.H * kHeadValues + e;

@@ -31,7 +31,7 @@ struct KPrefill {
 };
 
 // Segment slots: sequence s has slots cu[s] / seg + s and on, as many as segments.
-inline int64_t prefill_slots(int64_t rows, int64_t n, int64_t seg) { return rows / seg + n; }
+constexpr int64_t prefill_slots(int64_t rows, int64_t n, int64_t seg) { return rows / seg + n; }
 constexpr int kLeastSegment = 256;
 int prefill_segment(int64_t rows, int64_t n, int64_t heads);
 int64_t prefill_most_slots(int64_t rows, int64_t n, int64_t heads);

@@ -88,6 +88,26 @@ def test_slices_of_wider_rows_and_rows_nobody_owns():
     assert bool((out[rows - 45:] == -7).all())
 
 
+@pytest.mark.parametrize("n", [3, 63, 64, 129])
+def test_sequences_over_the_same_rows_write_nothing_outside(n):
+    """cu_seqlens that go to the last row and back: every other sequence has all rows, and their segments are more than
+    the slots."""
+    g = gen(n)
+    rows, H = 2000, 2
+    a = R.inputs(g, rows, H, 1)
+    cu = torch.tensor([rows * (i % 2) for i in range(n + 1)], dtype=torch.int32, device="cuda:0")
+    d = {k: t.to("cuda:0") for k, t in a.items()}
+    size = ssu.prefill_workspace_size(rows, n, H)
+    ws = torch.full((size + (64 << 20),), 0xA5, dtype=torch.uint8, device="cuda:0")
+    out = torch.full((rows + 64, H, 64), -7.0, device="cuda:0")
+    h1 = torch.full((n + 4, H, 64, 128), -7.0, device="cuda:0")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda:0")
+    ssu.prefill(ssu.make_prefill(cu, d["x"], d["B"], d["C"], d["dt"], d["A"], d["D"], d["dt_bias"], out[:rows], final_states=h1[:n],
+                                 workspace=ws[:size], status=status))
+    assert int(status) == ssu.SSU_STATUS_BAD_SEQLEN
+    assert bool((ws[size:] == 0xA5).all()) and bool((out[rows:] == -7).all()) and bool((h1[n:] == -7).all())
+
+
 def test_a_workspace_is_enough_for_fewer_rows_and_sequences():
     most = {}
     for H in (1, 4, 64, 129):
