@@ -91,8 +91,8 @@ int ssu_history_count(const ssu_history *history, const ssu_count_args *args, hi
  * temperature <= 0 (or NaN): p = 1 at the lowest i of the largest x.  In both x
  * = +inf counts as the largest finite value.  A row with no x above -inf is
  * all 0 and ORs SSU_STATUS_EMPTY_ROW.  With no_softmax the outputs are x /
- * temperature (x itself where that is <= 0 or NaN), rounded to out_dtype, and
- * nothing is said of empty rows.
+ * temperature (x itself where that is <= 0 or NaN; -inf stays -inf), rounded to
+ * out_dtype, and nothing is said of empty rows.
  *
  *   logits, out  [rows][vocab], logits_dtype / out_dtype (SSU_F32, SSU_BF16 or
  *                SSU_F16), rows *_row_stride ELEMENTS apart (at least vocab),

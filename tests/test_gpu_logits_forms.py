@@ -59,6 +59,16 @@ def test_greedy_rows(vocab, it):
     check(c, it)
 
 
+@pytest.mark.parametrize("temperature", [float("inf"), 0.5, 0.0])
+def test_what_is_left_out_stays_out_without_softmax(temperature):
+    c = Case(12, 3, 2, 3001, mask=0.5, temperature=[temperature] * 3)
+    c.wide[0, ::5] = float("nan")
+    c.wide[1, ::3] = -float("inf")
+    out = c.call("f32", softmax=False)[0]
+    x = torch.from_numpy(c.x())
+    assert torch.equal(out == -float("inf"), x == -float("inf")) and not bool(torch.isnan(out).any())
+
+
 @pytest.mark.parametrize("vocab", FORMS)
 def test_rows_that_a_mask_leaves_nothing_of(vocab):
     c = Case(3, 3, 2, vocab, mask=0.5)
