@@ -5,11 +5,11 @@
 //   W_ts = e^(G_t - G_s) dt'_s (C_t.B_s), + D on the diagonal,
 //   S' = e^(G_w) S + sum_s (e^(G_w - G_s) dt'_s x_s) B_s^T.
 // Everything but the exponentials is matrix products: a chunk and a head cost 128 (three
-// parts: 192) products of 16 x 16 x 32 for the readout, 192 for the update, 40 or 60 for the
-// tokens of the chunk and 40 for C.B, which the heads of a workgroup share.  Their operands
+// parts: 192) products of 16 x 16 x 32 for the readout, 192 for the update, 48 or 72 for the
+// tokens of the chunk and 64 for C.B, which the heads of a workgroup share.  Their operands
 // that are not bf16 have to be split into bf16 parts on the way, and that and the weights
-// cost the vector units as much again: 8 prompts of 2048 to 4096 tokens of 128 heads take
-// 400 us, 187 are their bytes, 125 the products alone.
+// cost the vector units more again: 8 prompts of 2048 to 4096 tokens of 128 heads take
+// 400 to 450 us with the clock, 186 are their bytes, 130 the products alone.
 // Two waves a head have 32 of its 64 columns each (or four have 16), the state in registers
 // as matrix results [n][p], which are the next product's operand as they lie.  B, C and x of a
 // chunk lie in LDS, the next chunk's on their way in registers.
@@ -17,7 +17,7 @@
 // Long sequences are cut into segments: prefill_kernel<.., true> forms what each
 // segment but the last adds to the state and its decay, segment_kernel the state that
 // each starts from, then all segments run at once (16384 tokens of 64 heads: 60, 13 and
-// 160 of 233 us).
+// 170 of 240 us).
 #include <stddef.h>
 
 #include <algorithm>
