@@ -11,11 +11,10 @@
  *   y_t = S C_t + D[h] x_t,  out_t = y_t  or  y_t z_t sigmoid(z_t)
  * A[h] dt' is at least -2^20 (exp is 0 from -104 on).  Everything between the
  * inputs and the outputs is computed in fp32 (decay sums in fp64); operands of
- * matrix products that are not bf16 enter them in three bf16 parts (24 bits)
- * or, where the result is rounded to bf16 anyway, in two.  Infinities or NaN
- * in a token's inputs may reach every output of the call for its sequence and
- * head (from B and C: of the heads of its group), the tokens before it too, and
- * nothing else.
+ * matrix products that are not bf16 enter them in three bf16 parts (24 bits).
+ * bf16 outputs are the fp32 ones rounded once.  Infinities or NaN in a token's
+ * inputs may reach every output of the call for its sequence and head (from B
+ * and C: of the heads of its group), the tokens before it too, and nothing else.
  *
  * The conventions of ssu.h hold: device pointers owned by the caller, nothing
  * allocated or synchronised, every kernel on the given stream of the current

@@ -4,12 +4,12 @@
 //   y_t = e^(G_t) C_t.S + sum_(s <= t) W_ts x_s,
 //   W_ts = e^(G_t - G_s) dt'_s (C_t.B_s), + D on the diagonal,
 //   S' = e^(G_w) S + sum_s (e^(G_w - G_s) dt'_s x_s) B_s^T.
-// Everything but the exponentials is matrix products: a chunk and a head cost 128 (three
-// parts: 192) products of 16 x 16 x 32 for the readout, 192 for the update, 48 or 72 for the
-// tokens of the chunk and 64 for C.B, which the heads of a workgroup share.  Their operands
-// that are not bf16 have to be split into bf16 parts on the way, and that and the weights
-// cost the vector units more again: 8 prompts of 2048 to 4096 tokens of 128 heads take
-// 400 to 450 us with the clock, 186 are their bytes, 130 the products alone.
+// Everything but the exponentials is matrix products: a chunk and a head cost 192 products of
+// 16 x 16 x 32 for the readout, 192 for the update, 72 for the tokens of the chunk and 64 for
+// C.B, which the heads of a workgroup share.  Their operands that are not bf16 have to be split
+// into three bf16 parts on the way, and that and the weights cost the vector units more again:
+// 8 prompts of 2048 to 4096 tokens of 128 heads take 470 us, 186 are their bytes, 157 the
+// products alone at 2.5 PFLOP/s.
 // Two waves a head have 32 of its 64 columns each (or four have 16), the state in registers
 // as matrix results [n][p], which are the next product's operand as they lie.  B, C and x of a
 // chunk lie in LDS, the next chunk's on their way in registers.
@@ -34,7 +34,9 @@ constexpr int kTiles = kT * (kT + 1) / 2;     // C.B tiles on and below the diag
 constexpr int kHeadValues = kHeadDim * kDState;
 constexpr int head_waves(int CT) { return kT / CT; }  // of a head, 16 CT columns each: they form the gates of as many chunks at once
 
-constexpr int out_parts(int OT) { return OT == kOutF32 ? 3 : 2; }
+// bf16 parts of an operand that is not bf16: 24 bits, whatever the outputs' type (with two towards bf16 ones the readout's
+// error of 2^-18 let five times as many of them round the other way).
+constexpr int kParts = 3;
 
 // [b0, b1) of sequence s; false where cu_seqlens is not what it has to be.
 __device__ __forceinline__ bool seq_rows(const KPrefill &p, int s, int &b0, int &b1) {
@@ -127,6 +129,8 @@ struct PBuf {
 // The pairs of a chunk's tiles of 16 tokens ti with tiles of 32 ks that hold tokens up to them.
 constexpr int kPairs = 6;
 constexpr int pair_at(int ti, int ks) { return (ti < 2 ? ti : 2 * ti - 2) + ks; }
+// A head's W of a chunk as the parts of operands: they take the place of C and x, which nobody reads any more by then.
+constexpr size_t kHeadWeights = kPairs * kParts * 64 * sizeof(bf16x8);
 
 // v of lane l
 __device__ __forceinline__ double lane_d(double v, int l) {
@@ -213,11 +217,8 @@ __device__ __forceinline__ bf16x8 x_tile(const uint16_t *x, int ks, int p, int l
   return __builtin_bit_cast(bf16x8, r);
 }
 
-// z sigmoid(z) times v.  Towards fp32: e^-z as 2 to an exact product of z (8 bits) and 15 bits of log2(e), times what
-// those leave.
-template <int OT>
+// z sigmoid(z) times v: e^-z as 2 to an exact product of z (8 bits) and 15 bits of log2(e), times what those leave.
 __device__ __forceinline__ float gated(float v, float z) {
-  if constexpr (OT != kOutF32) return v * z * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(z * -1.44269502f));
   const float hi = -z * 0x1.7154p+0f, lo = z * -0x1.d94aep-18f;  // log2(e) = 1.44268799 + 7.0526e-6
   const float e = __builtin_amdgcn_exp2f(hi);
   return v * z * __builtin_amdgcn_rcpf(1.f + fmaf(e, lo * 0.69314718f, e));
@@ -279,13 +280,14 @@ struct PStage {
 // token 16 ti + m in y[pt][ti][r].
 template <int OT, int HPW, int CT, bool STATE, bool GATE>
 __global__ __launch_bounds__(HPW * head_waves(CT) * 64, HPW * head_waves(CT) / 2) void prefill_kernel(KPrefill p, int htiles, int unit, int64_t ntiles) {
-  constexpr int NP = out_parts(OT), WPH = head_waves(CT), NT = HPW * WPH * 64;
+  constexpr int NP = kParts, WPH = head_waves(CT), NT = HPW * WPH * 64;
   typedef PBuf<HPW, STATE> Buf;
-  constexpr size_t kShareAt = offsetof(Buf, C);
-  constexpr bool SHARE = !STATE && kShareAt + HPW * kPairs * NP * 64 * sizeof(bf16x8) <= sizeof(Buf);
-  __shared__ Buf in;
+  constexpr size_t kWeightsAt = offsetof(Buf, C), kWeightsEnd = STATE ? 0 : kWeightsAt + HPW * kHeadWeights;
+  __shared__ __align__(16) uint8_t buf[sizeof(Buf) > kWeightsEnd ? sizeof(Buf) : kWeightsEnd];
+  Buf &in = *reinterpret_cast<Buf *>(buf);
   __shared__ __align__(16) Gates gates[HPW][WPH];
   __shared__ f32x4 cb[STATE ? 1 : kTiles][64];
+  static_assert(2 * (sizeof(buf) + sizeof(gates) + sizeof(cb)) <= 160 * 1024, "two workgroups a CU");
   const int tid = threadIdx.x, lane = tid & 63, m = lane & 15, q = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), hh = wave / WPH, wh = wave % WPH, p0 = wh * 16 * CT;
   if (!STATE) {
@@ -494,26 +496,23 @@ __global__ __launch_bounds__(HPW * head_waves(CT) * 64, HPW * head_waves(CT) / 2
           }
           split<NP>(w, wf);
         };
-        // Where there is room behind C (which nobody reads any more), a head's waves form a part of W each (16 prompts of
-        // 351 to 701 tokens, 32 heads, 75 -> 70 us; 8 of 2048 to 4096, 128 heads, gated, 491 -> 479).
-        bf16x8 *shared = reinterpret_cast<bf16x8 *>(reinterpret_cast<uint8_t *>(&in) + kShareAt) + hh * kPairs * NP * 64 + lane;
+        // A head's waves form a part of W each.
+        bf16x8 *shared = reinterpret_cast<bf16x8 *>(buf + kWeightsAt + hh * kHeadWeights) + lane;
         __syncthreads();
-        if constexpr (SHARE) {
-          auto form = [&](int ti) {
+        auto form = [&](int ti) {
 #pragma unroll
-            for (int ks = 0; ks <= ti / 2; ++ks) {
-              bf16x8 wf[NP];
-              weights(ti, ks, wf);
+          for (int ks = 0; ks <= ti / 2; ++ks) {
+            bf16x8 wf[NP];
+            weights(ti, ks, wf);
 #pragma unroll
-              for (int a = 0; a < NP; ++a) shared[(pair_at(ti, ks) * NP + a) * 64] = wf[a];
-            }
-          };
-          if (wh == 0) form(0);
-          if (wh == 1) form(1);
-          if (wh == (CT == 2 ? 1 : 2)) form(2);
-          if (wh == (CT == 2 ? 0 : 3)) form(3);
-          __syncthreads();
-        }
+            for (int a = 0; a < NP; ++a) shared[(pair_at(ti, ks) * NP + a) * 64] = wf[a];
+          }
+        };
+        if (wh == 0) form(0);
+        if (wh == 1) form(1);
+        if (wh == (CT == 2 ? 1 : 2)) form(2);
+        if (wh == (CT == 2 ? 0 : 3)) form(3);
+        __syncthreads();
         // the tokens of the chunk, and out
         const uint32_t och = (h * kHeadDim + p0 + 4 * q) * kOut;
 #pragma unroll
@@ -525,12 +524,8 @@ __global__ __launch_bounds__(HPW * head_waves(CT) * 64, HPW * head_waves(CT) / 2
 #pragma unroll
           for (int ks = 0; ks <= ti / 2; ++ks) {
             bf16x8 wf[NP];
-            if constexpr (SHARE) {
 #pragma unroll
-              for (int a = 0; a < NP; ++a) wf[a] = shared[(pair_at(ti, ks) * NP + a) * 64];
-            } else {
-              weights(ti, ks, wf);
-            }
+            for (int a = 0; a < NP; ++a) wf[a] = shared[(pair_at(ti, ks) * NP + a) * 64];
 #pragma unroll
             for (int a = NP - 1; a >= 0; --a)
 #pragma unroll
@@ -542,7 +537,7 @@ __global__ __launch_bounds__(HPW * head_waves(CT) * 64, HPW * head_waves(CT) / 2
               f32x4 v = y[pt][ti];
               if (GATE) {
 #pragma unroll
-                for (int r = 0; r < 4; ++r) v[r] = gated<OT>(v[r], bf2f((zw[pt][ti][r >> 1] >> (16 * (r & 1))) & 0xFFFFu));
+                for (int r = 0; r < 4; ++r) v[r] = gated(v[r], bf2f((zw[pt][ti][r >> 1] >> (16 * (r & 1))) & 0xFFFFu));
               }
               char *at = out + (uint32_t)(m * os + och + 16 * ti * os) + 16 * pt * kOut;
               if constexpr (OT == kOutF32)
