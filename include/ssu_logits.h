@@ -59,9 +59,9 @@ typedef struct ssu_history {
  * A token outside [0, vocab) is left out (SSU_STATUS_BAD_TOKEN); an entry whose
  * number is outside [0, max_seqlen], or whose cu_seqlens are negative,
  * decreasing or past rows, is skipped (SSU_STATUS_BAD_SEQLEN), its page left
- * as it is.  Requirements: batch <= 2^20, max_seqlen >= 1 without cu_seqlens
- * (ignored with them), rows >= batch * max_seqlen then; pointers 4-byte
- * aligned.  batch == 0 is a no-op; with rows == 0 tokens may be NULL.
+ * as it is.  Requirements: batch <= 2^20, rows <= 2^30, max_seqlen >= 1
+ * without cu_seqlens (ignored with them), rows >= batch * max_seqlen then;
+ * pointers 4-byte aligned.  batch == 0 is a no-op; with rows == 0 tokens may be NULL.
  */
 typedef struct ssu_count_args {
   int32_t batch, max_seqlen, rows;

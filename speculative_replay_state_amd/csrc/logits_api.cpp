@@ -27,6 +27,8 @@ int logit_type(int32_t t) {
   return t == SSU_F32 ? ssu::kLF32 : t == SSU_BF16 ? ssu::kLBF16 : t == SSU_F16 ? ssu::kLF16 : -1;
 }
 
+constexpr int32_t kMaxCountRows = 1 << 30;  // an index steps past an entry's last token by up to 4096
+
 int check_vocab(int32_t vocab) {
   if (vocab < 1) return api_fail(SSU_ERR_INVALID, "vocab must be positive (got %d)", vocab);
   if (vocab > (1 << 24)) return api_fail(SSU_ERR_UNSUPPORTED, "vocab %d exceeds 2^24", vocab);
@@ -101,6 +103,7 @@ int ssu_history_count(const ssu_history *history, const ssu_count_args *a, hipSt
   if (a->batch < 0) return api_fail(SSU_ERR_INVALID, "batch must be >= 0 (got %d)", a->batch);
   if (a->batch > (1 << 20)) return api_fail(SSU_ERR_UNSUPPORTED, "batch %d exceeds 2^20 entries per call", a->batch);
   if (a->rows < 0) return api_fail(SSU_ERR_INVALID, "rows must be >= 0 (got %d)", a->rows);
+  if (a->rows > kMaxCountRows) return api_fail(SSU_ERR_UNSUPPORTED, "rows %d exceeds 2^30", a->rows);
   if (!a->cu_seqlens && a->max_seqlen < 1) return api_fail(SSU_ERR_INVALID, "max_seqlen must be >= 1 (got %d)", a->max_seqlen);
   if (a->batch == 0) return api_ok();
   if (!a->slot_idx || (a->rows > 0 && !a->tokens)) return api_fail(SSU_ERR_INVALID, "slot_idx and tokens must not be NULL");
