@@ -172,6 +172,8 @@ def make_logits(logits, out, batch, max_seqlen, cu_seqlens=None, history=None, s
     workspace: at least logits_workspace_size(batch, max_seqlen, vocab) bytes
     (none without softmax)."""
     import torch
+    if bias_offsets is not None and (bias_tokens is None or bias_values is None):
+        raise ValueError("bias_offsets needs bias_tokens and bias_values")
     _shape(logits, "logits", (None, None))
     rows, vocab = logits.shape
     it, in_stride = _values(logits, "logits", rows, vocab)

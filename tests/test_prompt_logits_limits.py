@@ -1,7 +1,7 @@
-"""Limits of token histories and logits that are refused before any launch (CPU;
+"""What token histories and logits refuse before any launch (CPU;
 the pointers are never dereferenced)."""
 import pytest
-import torch  # noqa: F401  (before the library, which then shares its HIP runtime)
+import torch  # (before the library, which then shares its HIP runtime)
 
 import speculative_replay_state_amd as ssu
 from speculative_replay_state_amd import sampling
@@ -20,3 +20,9 @@ def test_counts_of_more_rows_than_an_index_steps_over(kw, rows):
 
 def test_counts_of_2_to_the_30_rows_are_no_refusal():
     assert sampling.ssu_history_count(_history(), _count(batch=0, rows=2 ** 30)) == ssu.SSU_OK
+
+
+@pytest.mark.parametrize("kw", [{}, dict(bias_tokens=torch.zeros(2, dtype=torch.int32)), dict(bias_values=torch.zeros(2))])
+def test_biases_need_tokens_and_values(kw):
+    with pytest.raises(ValueError, match="bias_tokens and bias_values"):
+        ssu.make_logits(torch.zeros(1, 64), torch.zeros(1, 64), 1, 1, bias_offsets=torch.zeros(2, dtype=torch.int32), **kw)
