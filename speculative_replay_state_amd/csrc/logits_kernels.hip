@@ -418,16 +418,18 @@ struct Stat {
   float m, s;
 };
 constexpr Stat kNoStat = {-INFINITY, 0.f};
-// log2(e) / temperature, finite and positive: (x - m) times it is 0 at x = m and -inf at x = -inf
+// 2 log2(e) / temperature, finite and positive: half of x - m times it is 0 at x = m and -inf at x = -inf
 __device__ __forceinline__ float slope(float temperature) {
-  return fminf(fmaxf(1.4426950408889634f / temperature, FLT_MIN), FLT_MAX);
+  return fminf(fmaxf(2.8853900817779268f / temperature, FLT_TRUE_MIN), FLT_MAX);
 }
+// half of x - m (all of it may be no finite number, and matters where the temperature is as large)
+__device__ __forceinline__ float half_of(float x, float m) { return fmaf(x, 0.5f, -0.5f * m); }
 __device__ __forceinline__ float finite(float x) { return fminf(fmaxf(x, -FLT_MAX), FLT_MAX); }
 // exp2 between 0 and 1, 0 of NaN: of x = +inf and the largest finite m 1.  (The bounds are the instruction's own.)
 __device__ __forceinline__ float exp_of(float d) { return __builtin_amdgcn_fmed3f(__builtin_amdgcn_exp2f(d), 0.f, 1.f); }
 __device__ __forceinline__ Stat join(Stat a, Stat b, float k) {
   const float m = fmaxf(a.m, b.m), M = finite(m);
-  return Stat{m, a.s * exp_of((a.m - M) * k) + b.s * exp_of((b.m - M) * k)};
+  return Stat{m, a.s * exp_of(half_of(a.m, M) * k) + b.s * exp_of(half_of(b.m, M) * k)};
 }
 template <int N>
 __device__ __forceinline__ void add_values(Stat &o, const float *v, float k) {
@@ -435,9 +437,9 @@ __device__ __forceinline__ void add_values(Stat &o, const float *v, float k) {
 #pragma unroll
   for (int e = 0; e < N; ++e) m = fmaxf(m, v[e]);
   const float M = finite(m);
-  float s = o.s * exp_of((o.m - M) * k);
+  float s = o.s * exp_of(half_of(o.m, M) * k);
 #pragma unroll
-  for (int e = 0; e < N; ++e) s += exp_of((v[e] - M) * k);
+  for (int e = 0; e < N; ++e) s += exp_of(half_of(v[e], M) * k);
   o.m = m;
   o.s = s;
 }
@@ -487,7 +489,7 @@ __device__ __forceinline__ Best block_best(Best s, Best *lds, int tid) {
 struct Probs {
   float M, k, inv;
   __device__ __forceinline__ Probs(Stat s, float slope) : M(finite(s.m)), k(slope), inv(s.m > -INFINITY ? 1.f / s.s : 0.f) {}
-  __device__ __forceinline__ float operator()(float x) const { return exp_of((x - M) * k) * inv; }
+  __device__ __forceinline__ float operator()(float x) const { return exp_of(half_of(x, M) * k) * inv; }
 };
 
 // Says so where an entry's biased tokens are none.
