@@ -378,24 +378,19 @@ __global__ __launch_bounds__(HPW * head_waves(CT) * 64, HPW * head_waves(CT) / 2
         for (int ks = 0; ks < 2; ++ks) xf[pt][ks] = x_tile(in.x[hh], ks, p0 + 16 * pt, lane);
       f32x4 y[CT][kT];
       if constexpr (!STATE) {
-        // The state's readout, and beside it C.B of token tiles si with all (those above the diagonal are not used).
-        // What a step reads from LDS is read a step ahead.
-        constexpr int NS = kT / (HPW * WPH);
-        int si[NS];
-#pragma unroll
-        for (int k = 0; k < NS; ++k) si[k] = k == 0 ? wave : 3 - wave;
-        f32x4 v[NS][kT];
+        // The state's readout, and beside it C.B of the wave's token tile with all (those above the diagonal are not
+        // used).  What a step reads from LDS is read a step ahead.
+        static_assert(HPW * WPH == kT, "a token tile of B a wave");
+        f32x4 v[kT];
 #pragma unroll
         for (int ti = 0; ti < kT; ++ti) {
 #pragma unroll
           for (int pt = 0; pt < CT; ++pt) y[pt][ti] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int k = 0; k < NS; ++k) v[k][ti] = f32x4{0.f, 0.f, 0.f, 0.f};
+          v[ti] = f32x4{0.f, 0.f, 0.f, 0.f};
         }
-        bf16x8 cf[2][kT], bf[2][NS];
+        bf16x8 cf[2][kT], bf[2];
         auto read = [&](int i) {
-#pragma unroll
-          for (int k = 0; k < NS; ++k) bf[i & 1][k] = row_frag(in.B, 16 * si[k], 32 * i, lane);
+          bf[i & 1] = row_frag(in.B, 16 * wave, 32 * i, lane);
 #pragma unroll
           for (int ti = 0; ti < kT; ++ti) cf[i & 1][ti] = row_frag(in.C, 16 * ti, 32 * i, lane);
         };
@@ -412,9 +407,7 @@ __global__ __launch_bounds__(HPW * head_waves(CT) * 64, HPW * head_waves(CT) / 2
             split<NP>(s, f[pt]);
           }
 #pragma unroll
-          for (int k = 0; k < NS; ++k)
-#pragma unroll
-            for (int ti = 0; ti < kT; ++ti) v[k][ti] = mfma_bf16(bf[i & 1][k], cf[i & 1][ti], v[k][ti]);
+          for (int ti = 0; ti < kT; ++ti) v[ti] = mfma_bf16(bf[i & 1], cf[i & 1][ti], v[ti]);
 #pragma unroll
           for (int a = NP - 1; a >= 0; --a)
 #pragma unroll
@@ -423,10 +416,8 @@ __global__ __launch_bounds__(HPW * head_waves(CT) * 64, HPW * head_waves(CT) / 2
               for (int pt = 0; pt < CT; ++pt) y[pt][ti] = mfma_bf16(f[pt][a], cf[i & 1][ti], y[pt][ti]);
         }
 #pragma unroll
-        for (int k = 0; k < NS; ++k)
-#pragma unroll
-          for (int ti = 0; ti < kT; ++ti)
-            if (ti >= si[k]) cb[ti * (ti + 1) / 2 + si[k]][lane] = v[k][ti];
+        for (int ti = 0; ti < kT; ++ti)
+          if (ti >= wave) cb[ti * (ti + 1) / 2 + wave][lane] = v[ti];
       }
       // S <- e^(G_w) S + B^T (w x)
       {
