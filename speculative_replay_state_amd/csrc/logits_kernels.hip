@@ -1,8 +1,10 @@
 // Token histories (ssu_history_count) and logits (ssu_logits).
 //
 // The softmax takes every value twice, for the largest x and the sum of exp((x - m) /
-// temperature), and for the probabilities; memory bounds it from some hundred rows on
-// (each value in and out once: a row stays in the caches between the two).  The values
+// temperature), and for the probabilities; memory bounds it from some hundred rows on.
+// The first values of a row stay in registers between the two; the others come again, from
+// the last cache where the rows under way are more than an L2 holds (64 of them an XCD: of
+// 131072 bf16 values 16 MiB for 4, and 995 MiB are read for 442 of logits and masks).  They
 // go through registers 8 neighbours a lane, with a byte of a bitmap in LDS that says
 // which of them are not taken as they are: these become NaN, which counts for nothing
 // (a maximum passes over it, the exponential's own bounds of 0 and 1 make it 0; so a
@@ -10,8 +12,8 @@
 // the drafts or biased are special: a workgroup lists the special tokens of its range, a
 // thread each forms their x (the loads of the logit and of the count on their way at
 // once), and each is added to the sums and written by itself, behind the rest.  With a
-// copy of the row in registers and a third of the waves in its place 1536 rows of 131072
-// bf16 values took 329 us for 276 now, 194 without history, biases and masks; 176 is what
+// copy of the row in registers and a third of the waves in its place 1663 rows of 131072
+// bf16 values took 329 us for 281 now, 194 without history, biases and masks; 176 is what
 // the bytes take at a copy's 5.12 TB/s.
 #include "logits_internal.h"
 #include "ssu_device.cuh"
@@ -97,8 +99,9 @@ __global__ __launch_bounds__(NT) void count_kernel(KHistory h, KCount c) {
 
 // A prompt's tokens, each counted once: a workgroup per entry collects their bits in
 // LDS, as many words as there are, and adds them to the page without an atomic (a
-// text's frequent tokens share a few words: with one for each token 32 prompts of 2048 to
-// 4096 took 46 us).
+// text's frequent tokens share a few words: 32 prompts of 2048 to 4096 tokens take 11 us,
+// and 48 in count_kernel, which has an atomic for each token and takes the vocabularies
+// of more words than there are here).
 constexpr int kPromptWords = 4096;
 template <int NT>
 __global__ __launch_bounds__(NT) void count_prompt_kernel(KHistory h, KCount c) {
@@ -591,10 +594,13 @@ __global__ __launch_bounds__(kPieceThreads) void logits_piece_kernel(KHistory h,
 }
 
 // A whole row by one workgroup, two of 16 waves a CU: enough loads on their way while the other one lists its special
-// tokens.  The first HOLD groups of 8 values a thread are loaded before anything else and stay in registers, the others
-// are read AHEAD at a time, and for the second time from the caches.  (512 threads and 16 groups held took 318 us for 289 with
-// 1536 rows of 131072, one group at a time 304.)  ALONE: no more rows than CUs, and twice the registers for loads on
+// tokens.  The first HOLD groups of 8 values a thread are loaded once the special ones are marked and stay in registers, the
+// others are read AHEAD at a time, and for the second time from the caches.  (512 threads and 16 groups held took 318 us for
+// 289 with 1663 rows of 131072, one group at a time 304.)  ALONE: no more rows than CUs, and twice the registers for loads on
 // their way (256 rows of 100003 fp32 values that no cache holds 75 -> 63 us; 16-bit ones the same as without).
+// Two workgroups a CU leave room for the bitmaps and lists of 131072 values (72 KiB each).  Longer rows go by pieces, however
+// many they are, which reads them once more and lists their special tokens twice (bf16, history, masks, biases: 256 rows of
+// 131072 values 50 us, of 151936 135).
 constexpr int kRowThreads = 1024, kRowMax = 131072, kAlone = 256;
 
 template <int IT, int OT, bool ALONE>

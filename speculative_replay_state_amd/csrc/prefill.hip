@@ -8,16 +8,18 @@
 // 16 x 16 x 32 for the readout, 192 for the update, 72 for the tokens of the chunk and 64 for
 // C.B, which the heads of a workgroup share.  Their operands that are not bf16 have to be split
 // into three bf16 parts on the way, and that and the weights cost the vector units more again:
-// 8 prompts of 2048 to 4096 tokens of 128 heads take 470 us, 186 are their bytes, 157 the
-// products alone at 2.5 PFLOP/s.
+// 8 prompts of 2048 to 4096 tokens of 128 heads take 475 us, 186 are their bytes, 157 the
+// products alone at 2.5 PFLOP/s; matrix units are busy for 35 % of it, vector units for 38, and
+// the two waves of a SIMD issue for 35 % of theirs, wait for a busy unit or a result for 43, and
+// for loads and barriers for 21.
 // Two waves a head have 32 of its 64 columns each (or four have 16), the state in registers
 // as matrix results [n][p], which are the next product's operand as they lie.  B, C and x of a
 // chunk lie in LDS, the next chunk's on their way in registers.
 //
 // Long sequences are cut into segments: prefill_kernel<.., true> forms what each
 // segment but the last adds to the state and its decay, segment_kernel the state that
-// each starts from, then all segments run at once (16384 tokens of 64 heads: 60, 13 and
-// 170 of 240 us).
+// each starts from, then all segments run at once (16384 tokens of 64 heads, gated: 65, 13 and
+// 188 of 263 us).
 #include <stddef.h>
 
 #include <algorithm>
@@ -617,8 +619,8 @@ hipError_t prefill_t(const KPrefill &p, int out_type, hipStream_t st) {
 }  // namespace
 
 // Tokens of a segment: as many as leave two workgroups of two heads to each CU, and at least so many that the pass before
-// it pays: 256 where there are few workgroups (one prompt of 64 heads, 384 : 256: 2000 tokens 68 : 58 us, 4000 100 : 85), more
-// otherwise (16 of 351 to 701 tokens, 32 heads, 75 : 96; 8 of them 57 : 75; 4 of them 53 : 54).
+// it pays: 256 where there are few workgroups (one prompt of 64 heads, 384 : 256: 2000 tokens 59 : 50 us, 4000 95 : 80), more
+// otherwise (16 of 351 to 701 tokens, 32 heads, 61 : 81; 12 of them 51 : 90; 8 of them 49 : 72; 4 of them 48 either way).
 int prefill_segment(int64_t rows, int64_t n, int64_t heads) {
   const int64_t pairs = (heads + 1) / 2, want = (rows * pairs + 511) / 512, least = n * pairs <= 64 ? kLeastSegment : 384;
   return (int)((std::max<int64_t>(want, least) + kPChunk - 1) / kPChunk * kPChunk);
@@ -631,8 +633,9 @@ int64_t prefill_most_slots(int64_t rows, int64_t n, int64_t heads) {
 
 // Two heads a workgroup, which share B, C and their products, two waves of 32 columns each; where a CU would have no more
 // than one of those, and where a group has one head, a workgroup a head, four waves of 16 columns: one prompt of 500 tokens,
-// 64 heads, 49 : 35 us, 12 of 351 to 701 tokens, 32 heads, 75 : 58, 16 of them (256 workgroups of two heads) 80 : 70.
-// (Workgroups of one head of two waves: 8 prompts of 500 to 1000 tokens, 64 heads of 64 groups, 155 us for 138.)
+// 64 heads, 50 : 33 us, 12 of 351 to 701 tokens, 32 heads, 73 : 51, 16 of them (256 workgroups of two heads) 75 : 61; one of
+// 4000 tokens, 64 heads (512 of them), 80 : 87.  (Workgroups of one head of two waves took 155 us for 138 with 8 prompts of
+// 500 to 1000 tokens, 64 heads of 64 groups, and operands of two parts.)
 hipError_t launch_prefill(const KPrefill &p, int out_type, hipStream_t st) {
   if (p.hpg < 2) return prefill_t<1, 1>(p, out_type, st);
   const int64_t each = (p.rows + p.n - 1) / p.n, segments = each <= 2 * (int64_t)p.seg ? 1 : (each + p.seg - 1) / p.seg;

@@ -1,8 +1,8 @@
 // Checkpoints as fp32 states (ssu_read_state).
 //
 // A wave takes a row block of 16 rows; a lane 4 neighbouring values of a row,
-// so that a store instruction writes 1 KiB in one piece: the stores are 2 to 8
-// times the bytes of the loads, which find the row block's other lines in
+// so that a store instruction writes 1 KiB in one piece: the stores are as many bytes as
+// the loads (fp32) to 8 times as many, and the loads find the row block's other lines in
 // the CU's cache.  HBM bounds it: 64 slots of 128 heads of fp8, 338 MB, take 66 us, a
 // copy's 5.1 TB/s; one slot of 16 heads takes 3.0.
 #include "prefill_internal.h"
